@@ -219,7 +219,7 @@ def _rowwise4(x):
     v, b = _scaled(x.float().unflatten(1, (-1, 32)), 2, 0.75, 3)
     m = v.abs().nan_to_num(nan=6.0)
     c = ((m > 0.25).byte() + (m >= 0.75) + (m > 1.25) + (m >= 1.75) + (m > 2.5) + (m >= 3.5)
-         + (m > 5.0) + 8 * (torch.signbit(v) & ~v.isnan()))
+         + (m > 5.0) + 8 * (torch.signbit(v) & ~v.isnan()).byte())
     c = c.flatten(1)
     return c[:, 0::2] | (c[:, 1::2] << 4), b
 
