@@ -366,13 +366,14 @@ moeact_status moeact_clamped_sigmoid_dump(float alpha, float limit, float* out, 
  * timer), and the kernel then waits (bounded again) for its copies in flight
  * and returns, its outputs incomplete.  Bit 4 is set only by
  * moeact_wait_selftest; bit 5 by the fused FC2 kernel
- * (grouped_scaled_swiglu_mxfp8_fc2).  Synchronous.  No counterpart on the pages. */
+ * (grouped_scaled_swiglu_mxfp8_fc2); bit 6 by the grouped products.  Synchronous.  No counterpart on the pages. */
 #define MOEACT_DEVERR_FWD_WAIT 0x1u
 #define MOEACT_DEVERR_BWD_WAIT 0x2u
 #define MOEACT_DEVERR_TABLE_WAIT 0x4u
 #define MOEACT_DEVERR_TABLE_ADDR 0x8u
 #define MOEACT_DEVERR_WAIT_SELFTEST 0x10u
 #define MOEACT_DEVERR_FC2_WAIT 0x20u
+#define MOEACT_DEVERR_GEMM_WAIT 0x40u
 moeact_status moeact_device_error(uint32_t* flags);
 
 /* ---------------------------------------------------------------------
@@ -432,6 +433,111 @@ moeact_status grouped_scaled_swiglu_mxfp8_fc2(const void* x, int64_t ldx, const 
                                               const void* w_scales, int64_t H, void* out,
                                               int64_t ldo, const int32_t* noop_flag,
                                               void* stream);
+
+/* ---------------------------------------------------------------------
+ * mxfp8_quantize, grouped_mxfp8_quantize -- the plain MXFP8 of bf16 rows: the
+ * operands of the grouped products below (the tokens of an expert's first
+ * linear layer, an output gradient, a weight).  Numerics, layouts, directions,
+ * groups and errors are those of the forward calls above with y = x: no
+ * activation and no row scale.  x bf16 [M, ldx], ldx >= N.  A weight of E
+ * experts is quantized as one dense [E * H, K] matrix; with H a multiple of
+ * 32 no 32-row block of its colwise direction crosses an expert.
+ * ------------------------------------------------------------------- */
+moeact_status mxfp8_quantize(const void* x, int64_t ldx, int64_t M, int64_t N, int dirs,
+                             moeact_mx_out out, void* stream);
+moeact_status grouped_mxfp8_quantize(const void* x, int64_t ldx, int64_t M, int64_t N, int dirs,
+                                     const int64_t* row_offs, const int64_t* colblk_offs,
+                                     int32_t num_groups, int32_t* status, moeact_mx_out out,
+                                     void* stream);
+
+/* ---------------------------------------------------------------------
+ * mxfp4_quantize, mxfp4_dequantize -- MXFP4 (OCP MX: E2M1 codes, E8M0 scales)
+ * of bf16 rows in 1 x 32 blocks, and the bf16 values it stands for.
+ *   E8M0  b = 127 + e, e the smallest integer in [-127, 127] with
+ *         amax <= 6 * 2^e (RCEIL; +Inf -> 254, NaN -> 255).
+ *   E2M1  nearest-even code of x * 2^(127-b), saturating to +-6, sign of zero
+ *         kept; a block with b = 255 has all codes 7.
+ *   codes  uint8 [M, N/2], column 2j in the low four bits of byte j;
+ *   scales uint8 [M, N/32] in `scale_layout` (MOEACT_SCALES_GEMM: M and N
+ *          multiples of 128).
+ *   The dequantizer writes code * 2^(b-127), exact in bf16 (an overflow is
+ *   infinite; b = 255 gives NaN).
+ * N a positive multiple of 32; x / out rows at a stride of ldx / ldo >= N
+ * elements, a multiple of 8; every pointer 16-byte aligned.  M == 0 returns
+ * MOEACT_OK without launching.  noop_flag as in moeact_mx_out.
+ * ------------------------------------------------------------------- */
+moeact_status mxfp4_quantize(const void* x, int64_t ldx, int64_t M, int64_t N, void* codes,
+                             void* scales, int32_t scale_layout, const int32_t* noop_flag,
+                             void* stream);
+moeact_status mxfp4_dequantize(const void* codes, const void* scales, int32_t scale_layout,
+                               int64_t M, int64_t N, void* out, int64_t ldo,
+                               const int32_t* noop_flag, void* stream);
+
+/* ---------------------------------------------------------------------
+ * Grouped products of block-scaled operands, on the tensor cores.  Group e
+ * owns rows [row_offs[e], row_offs[e+1]) (any count, zero included):
+ *   grouped_mxfp8_gemm   out[i, h] = sum_k A[i, k] W_e[h, k]
+ *   grouped_mxfp4_gemm   the same, both operands MXFP4
+ *   grouped_mxfp8_dgrad  dx[i, k]  = sum_h dY[i, h] W_e[h, k]
+ *   grouped_mxfp8_wgrad  dW_e[h, k] = sum_i dY[i, h] X[i, k]  (i over group e)
+ * for row i of group e, of the values the codes and scales stand for.
+ * Products are summed in fp32 by the tensor cores (order not specified); the
+ * sum is rounded once to the output type.  A NaN scale or code makes the
+ * outputs it enters NaN.
+ *   A, dY (gemm, dgrad)  rowwise codes [M, K] (dgrad [M, H]; MXFP4: [M, K/2]
+ *             bytes) and scales [M, K/32] ([M, H/32]) in their scale layout.
+ *   W (gemm)  rowwise codes and scales of the dense [E * H, K] matrix.
+ *   W (dgrad) colwise codes and scales of the same dense matrix (scales
+ *             [E * H / 32, K], or the tiled [K, E * H / 32] matrix).
+ *   dY, X (wgrad)  colwise codes [M, H] / [M, K] and scales as the grouped
+ *             quantizer and activation calls write them for these row_offs
+ *             and colblk_offs, both in the same scale layout; scale_rows: the
+ *             rows of W bytes that each scale array holds (colblk_offs[E] above
+ *             it is MOEACT_DEV_BAD_OFFSETS).
+ *   H, K      positive multiples of 32 (MOEACT_EINVAL), E * H < 2^31
+ *             (MOEACT_ERANGE).
+ *   scale layouts  MOEACT_SCALES_ROWMAJOR, or MOEACT_SCALES_GEMM (M, H and K
+ *             multiples of 128, MOEACT_EINVAL; in wgrad every group's rows
+ *             too, else status MOEACT_DEV_UNALIGNED_GROUPS).
+ *   out       bf16 or fp32 (out_dtype), rows at a stride of ldo >= the width,
+ *             a multiple of 16 bytes; columns past the width are not touched.
+ *             wgrad: dw [E, H, K] contiguous; groups without rows get zeros;
+ *             accumulate = 1 (fp32 only) adds to what dw holds.
+ *   status    int32 (device): MOEACT_DEV_OK, or MOEACT_DEV_BAD_OFFSETS /
+ *             MOEACT_DEV_UNALIGNED_GROUPS, in which case nothing is written.
+ * Every pointer 16-byte aligned (offsets 8, status and noop_flag 4), else
+ * MOEACT_EALIGN.  M == 0: gemm and dgrad launch nothing and leave the status
+ * word alone; wgrad writes its zeros.  Allocates nothing, keeps no workspace; asynchronous on `stream`.
+ * Bounded waits report MOEACT_DEVERR_GEMM_WAIT.
+ * ------------------------------------------------------------------- */
+#define MOEACT_OUT_BF16 0
+#define MOEACT_OUT_FP32 1
+moeact_status grouped_mxfp8_gemm(const void* a_codes, const void* a_scales,
+                                 int32_t a_scale_layout, int64_t M, int64_t K,
+                                 const int64_t* row_offs, int32_t num_groups, int32_t* status,
+                                 const void* w_codes, const void* w_scales,
+                                 int32_t w_scale_layout, int64_t H, void* out, int64_t ldo,
+                                 int32_t out_dtype, const int32_t* noop_flag, void* stream);
+moeact_status grouped_mxfp8_dgrad(const void* dy_codes, const void* dy_scales,
+                                  int32_t dy_scale_layout, int64_t M, int64_t H,
+                                  const int64_t* row_offs, int32_t num_groups, int32_t* status,
+                                  const void* w_codes, const void* w_scales,
+                                  int32_t w_scale_layout, int64_t K, void* dx, int64_t lddx,
+                                  int32_t out_dtype, const int32_t* noop_flag, void* stream);
+moeact_status grouped_mxfp8_wgrad(const void* dy_codes, const void* dy_scales,
+                                  const void* x_codes, const void* x_scales,
+                                  int64_t scale_rows, int32_t scale_layout, int64_t M, int64_t H,
+                                  int64_t K,
+                                  const int64_t* row_offs, const int64_t* colblk_offs,
+                                  int32_t num_groups, int32_t* status, void* dw,
+                                  int32_t out_dtype, int accumulate, const int32_t* noop_flag,
+                                  void* stream);
+moeact_status grouped_mxfp4_gemm(const void* a_codes, const void* a_scales,
+                                 int32_t a_scale_layout, int64_t M, int64_t K,
+                                 const int64_t* row_offs, int32_t num_groups, int32_t* status,
+                                 const void* w_codes, const void* w_scales,
+                                 int32_t w_scale_layout, int64_t H, void* out, int64_t ldo,
+                                 int32_t out_dtype, const int32_t* noop_flag, void* stream);
 
 /* ---------------------------------------------------------------------
  * moeact_wait_selftest -- checks the bounded wait of the fused kernels on the

@@ -19,7 +19,8 @@ ROWWISE, COLWISE = 1, 2
 DEV_OK, DEV_NEGATIVE_SPLIT, DEV_SPLIT_SUM, DEV_BAD_OFFSETS, DEV_UNALIGNED_GROUPS = range(5)
 SCALES_ROWMAJOR, SCALES_GEMM = 0, 1
 DEVERR_FWD_WAIT, DEVERR_BWD_WAIT, DEVERR_TABLE_WAIT, DEVERR_TABLE_ADDR = 0x1, 0x2, 0x4, 0x8
-DEVERR_WAIT_SELFTEST, DEVERR_FC2_WAIT = 0x10, 0x20
+DEVERR_WAIT_SELFTEST, DEVERR_FC2_WAIT, DEVERR_GEMM_WAIT = 0x10, 0x20, 0x40
+OUT_BF16, OUT_FP32 = 0, 1
 MAX_GROUPS = 2040
 
 
@@ -76,6 +77,15 @@ _SIGS = {
     "moeact_wait_selftest": ([I, ctypes.c_uint32, P, P], I),
     "grouped_scaled_swiglu_mxfp8_fc2": ([P, I64, P, I64, I64, I, P, I32, P, P, P, I64, P, I64, P,
                                          P], I),
+    "mxfp8_quantize": ([P, I64, I64, I64, I, MxOut, P], I),
+    "grouped_mxfp8_quantize": ([P, I64, I64, I64, I, P, P, I32, P, MxOut, P], I),
+    "mxfp4_quantize": ([P, I64, I64, I64, P, P, I32, P, P], I),
+    "mxfp4_dequantize": ([P, P, I32, I64, I64, P, I64, P, P], I),
+    "grouped_mxfp8_gemm": ([P, P, I32, I64, I64, P, I32, P, P, P, I32, I64, P, I64, I32, P, P], I),
+    "grouped_mxfp8_dgrad": ([P, P, I32, I64, I64, P, I32, P, P, P, I32, I64, P, I64, I32, P, P],
+                            I),
+    "grouped_mxfp8_wgrad": ([P, P, P, P, I64, I32, I64, I64, I64, P, P, I32, P, P, I32, I, P, P], I),
+    "grouped_mxfp4_gemm": ([P, P, I32, I64, I64, P, I32, P, P, P, I32, I64, P, I64, I32, P, P], I),
     "scaled_swiglu_mxfp8_bwd_noalloc": ([P, I64, P, I64, P, I64, I64, I, P, P, MxOut, P], I),
 }
 

@@ -15,7 +15,9 @@
 
 #include "../../include/moeact.h"
 #include "fc2.cuh"
+#include "grouped_gemm.cuh"
 #include "host_kernels.cuh"
+#include "mxfp4.cuh"
 #include "variants.cuh"
 
 namespace moeact {
@@ -47,9 +49,9 @@ std::mutex g_mu;
 __device__ int g_sigma_uncertain;
 __device__ uint32_t g_smem_base;
 
-// The fused kernels of each activation (index kSwiGLU / kSReLU / kClamped),
-// filled once.
-FwdVariant g_fwd[3][kFwdSlots];
+// The fused kernels of each activation (index kSwiGLU / kSReLU / kClamped, the
+// plain quantizers kPlain), filled once.
+FwdVariant g_fwd[4][kFwdSlots];
 BwdVariant g_bwd[3][kBwdSlots];
 bool g_tables_filled = false;
 
@@ -111,6 +113,8 @@ moeact_status init_device(int dev) {
     fill_fwd_clamped_ilv_grouped(g_fwd[kClamped]);
     fill_bwd_clamped_dense(g_bwd[kClamped]);
     fill_bwd_clamped_grouped(g_bwd[kClamped]);
+    fill_fwd_plain_dense(g_fwd[kPlain]);
+    fill_fwd_plain_grouped(g_fwd[kPlain]);
     g_tables_filled = true;
   }
   for (auto& tab : g_fwd)
@@ -132,6 +136,8 @@ moeact_status init_device(int dev) {
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
   e = fc2_prepare();
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute (fused FC2)");
+  e = grouped_gemm_prepare();
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute (grouped products)");
   e = cudaGetSymbolAddress(reinterpret_cast<void**>(&g_err_ptr[dev]), g_err_word);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetSymbolAddress");
   e = cudaGetSymbolAddress(reinterpret_cast<void**>(&g_sig_ptr[dev]), g_sigma_table);
@@ -229,12 +235,13 @@ moeact_status check_layout(const moeact_mx_out& o, int64_t M, int64_t N) {
 
 moeact_status check_shape(const void* x, int64_t ldx, const float* s, int64_t M, int64_t N,
                           int act) {
-  if (!x || !s) return fail(MOEACT_EINVAL, "x and s are required");
+  if (!x) return fail(MOEACT_EINVAL, "x is required");
+  if (!s && act != kPlain) return fail(MOEACT_EINVAL, "s is required");
   if (M < 0) return fail(MOEACT_EINVAL, "M must be >= 0 (got %lld)", (long long)M);
   if (N <= 0 || N % 32 != 0) return fail(MOEACT_EINVAL, "N must be a positive multiple of 32 (got %lld)", (long long)N);
   if (M > MOEACT_MAX_ROWS) return fail(MOEACT_ERANGE, "M above 2^30");
   if (N > (1 << 24)) return fail(MOEACT_ERANGE, "N above 2^24");
-  const int64_t width = act != kSReLU ? 2 * N : N;
+  const int64_t width = act != kSReLU && act != kPlain ? 2 * N : N;
   if (ldx < width) return fail(MOEACT_EINVAL, "ldx (%lld) smaller than the input width %lld", (long long)ldx, (long long)width);
   if (ldx % 8 != 0) return fail(MOEACT_EALIGN, "ldx must be a multiple of 8 elements");
   if (ldx > (((int64_t)1) << 40) || M * ldx > (((int64_t)1) << 61)) return fail(MOEACT_ERANGE, "input extent too large");
@@ -312,6 +319,23 @@ moeact_status make_map_ilv(CUtensorMap* map, const void* base, int64_t N, int64_
   const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
                               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(MOEACT_ECUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return MOEACT_OK;
+}
+
+// Tensor map of a code matrix of `rows` rows of `bytes` bytes (contiguous), in
+// boxes of 128 bytes x box_rows rows, 128-byte swizzled (the tensor cores'
+// operand layout); bytes outside read as zero.
+moeact_status make_code_map(CUtensorMap* map, const void* base, int64_t bytes, int64_t rows,
+                            int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)bytes, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)bytes};
+  const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
+                              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(MOEACT_ECUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return MOEACT_OK;
@@ -533,7 +557,7 @@ moeact_status fwd_common(const ActArgs& a, const void* x, int64_t ldx, const flo
   if (!v.fn) return fail(MOEACT_EUNSUPPORTED, "no forward kernel for this combination");
   CUtensorMap tx;
   if (ilv) st = make_map_ilv(&tx, x, N, ilv, M, ldx);
-  else st = make_map(&tx, x, act != kSReLU ? 2 * N : N, M, ldx);
+  else st = make_map(&tx, x, act != kSReLU && act != kPlain ? 2 * N : N, M, ldx);
   if (st) return st;
   const int64_t blocks = grid_for(slabs_upper, p.n_tiles, v.threads, dev);
   v.fn<<<(unsigned)blocks, v.threads, v.smem_fixed + group_smem(v.sig, grouped, p.E), cs>>>(tx, p);
@@ -626,7 +650,167 @@ moeact_status bwd_common(const ActArgs& a, const void* dy, int64_t lddy, const v
   return MOEACT_OK;
 }
 
+// ------------------------------------------------------------ MXFP4
+moeact_status check_scale_layout(int32_t layout, const char* name, int64_t rows, int64_t width) {
+  if (layout != MOEACT_SCALES_ROWMAJOR && layout != MOEACT_SCALES_GEMM)
+    return fail(MOEACT_EINVAL, "%s must be MOEACT_SCALES_ROWMAJOR or MOEACT_SCALES_GEMM", name);
+  if (layout == MOEACT_SCALES_GEMM && (rows % 128 != 0 || width % 128 != 0))
+    return fail(MOEACT_EINVAL, "the GEMM scale layout needs rows and widths that are multiples of "
+                "128 (got %lld, %lld)", (long long)rows, (long long)width);
+  return MOEACT_OK;
+}
+
+moeact_status check_width(int64_t w, const char* name) {
+  if (w <= 0 || w % 32 != 0)
+    return fail(MOEACT_EINVAL, "%s must be a positive multiple of 32 (got %lld)", name, (long long)w);
+  if (w > (1 << 24)) return fail(MOEACT_ERANGE, "%s above 2^24", name);
+  return MOEACT_OK;
+}
+
+moeact_status mxfp4_common(const void* x, int64_t ldx, int64_t M, int64_t N, void* codes,
+                           void* scales, int32_t layout, const int32_t* noop, void* stream,
+                           bool back) {
+  t_err[0] = 0;
+  const char* name = back ? "out" : "x";
+  if (M < 0) return fail(MOEACT_EINVAL, "M must be >= 0 (got %lld)", (long long)M);
+  moeact_status st = check_width(N, "N");
+  if (st) return st;
+  if (M > MOEACT_MAX_ROWS) return fail(MOEACT_ERANGE, "M above 2^30");
+  if ((st = check_scale_layout(layout, "scale_layout", M, N))) return st;
+  if (M == 0) return MOEACT_OK;
+  if (!x || !codes || !scales) return fail(MOEACT_EINVAL, "%s, codes and scales are required", name);
+  if (ldx < N) return fail(MOEACT_EINVAL, "row stride of %s (%lld) smaller than N", name, (long long)ldx);
+  if (ldx % 8 != 0) return fail(MOEACT_EALIGN, "row stride of %s must be a multiple of 8 elements", name);
+  if (ldx > (((int64_t)1) << 40) || M * ldx > (((int64_t)1) << 61))
+    return fail(MOEACT_ERANGE, "extent of %s too large", name);
+  if (ceil_div(M, 4) * ceil_div(N, 256) > INT32_MAX)
+    return fail(MOEACT_ERANGE, "more than 2^31 - 1 pieces of 4 rows x 256 columns");
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 16))
+    return fail(MOEACT_EALIGN, "%s, codes and scales must be 16-byte aligned", name);
+  if (noop && !aligned(noop, 4)) return fail(MOEACT_EALIGN, "noop_flag must be 4-byte aligned");
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  int dev;
+  if ((st = ensure_ready(cs, &dev))) return st;
+  Mxfp4Params p{};
+  p.x = static_cast<uint16_t*>(const_cast<void*>(x));
+  p.ldx = ldx;
+  p.M = M;
+  p.K = (int)N;
+  p.codes = static_cast<uint8_t*>(codes);
+  p.scales = static_cast<uint8_t*>(scales);
+  p.tiled = layout == MOEACT_SCALES_GEMM;
+  p.noop = noop;
+  const cudaError_t e = back ? mxfp4_dequantize_launch(p, g_sms[dev], cs)
+                             : mxfp4_quantize_launch(p, g_sms[dev], cs);
+  if (e != cudaSuccess) return cuda_fail(e, "MXFP4 launch");
+  return MOEACT_OK;
+}
+
+// ------------------------------------------------------------ grouped products
+moeact_status check_gemm_common(int64_t M, const int64_t* ro, int32_t E, int32_t* status,
+                                int32_t out_dtype, const int32_t* noop) {
+  if (M < 0) return fail(MOEACT_EINVAL, "M must be >= 0 (got %lld)", (long long)M);
+  if (M > MOEACT_MAX_ROWS) return fail(MOEACT_ERANGE, "M above 2^30");
+  if (!ro || !status) return fail(MOEACT_EINVAL, "row_offs and status are required");
+  if (E < 1 || E > MOEACT_MAX_GROUPS) return fail(MOEACT_EINVAL, "num_groups must be in [1, %d]", MOEACT_MAX_GROUPS);
+  if (!aligned(ro, 8) || !aligned(status, 4)) return fail(MOEACT_EALIGN, "row_offs must be 8-byte aligned, status 4-byte aligned");
+  if (out_dtype != MOEACT_OUT_BF16 && out_dtype != MOEACT_OUT_FP32)
+    return fail(MOEACT_EINVAL, "out_dtype must be MOEACT_OUT_BF16 or MOEACT_OUT_FP32");
+  if (noop && !aligned(noop, 4)) return fail(MOEACT_EALIGN, "noop_flag must be 4-byte aligned");
+  return MOEACT_OK;
+}
+
+// Whether a product runs on SM pairs (256 x 256 tiles) or on single SMs (128 x
+// 128): pairs where the rows fill their tiles and the tiles fill the pairs.
+bool gemm_pair(int64_t row_tiles, int64_t col_tiles, int64_t rows_per_group, int dev) {
+  return rows_per_group >= 128 && row_tiles * col_tiles >= g_sms[dev] / 2;
+}
+
+// Forward and dgrad: rows of A [M, K] times each group's W, rows of K
+// (forward: N of them per group) or rows of N (dgrad: K of them).
+moeact_status gemm_rows(int op, const void* a_codes, const void* a_scales, int32_t a_layout,
+                        int64_t M, int64_t K, const int64_t* ro, int32_t E, int32_t* status,
+                        const void* w_codes, const void* w_scales, int32_t w_layout, int64_t N,
+                        void* out, int64_t ldo, int32_t out_dtype, const int32_t* noop,
+                        void* stream) {
+  t_err[0] = 0;
+  moeact_status st = check_gemm_common(M, ro, E, status, out_dtype, noop);
+  if (st) return st;
+  const bool dgrad = op == kGemmDgrad;
+  const char* kn = dgrad ? "H" : "K";
+  const char* nn = dgrad ? "K" : "H";
+  if ((st = check_width(K, kn)) || (st = check_width(N, nn))) return st;
+  const int64_t wrows = (int64_t)E * (dgrad ? K : N);
+  if (wrows > INT32_MAX) return fail(MOEACT_ERANGE, "num_groups * H above 2^31 - 1");
+  if ((st = check_scale_layout(a_layout, "scale layout of the rows", M, K))) return st;
+  if (w_layout == MOEACT_SCALES_GEMM && (K % 128 != 0 || N % 128 != 0))
+    return fail(MOEACT_EINVAL, "the GEMM scale layout of w needs H and K to be multiples of 128");
+  if ((st = check_scale_layout(w_layout, "scale layout of w", 0, 128))) return st;
+  if (M == 0) return MOEACT_OK;
+  if (!a_codes || !a_scales || !w_codes || !w_scales || !out)
+    return fail(MOEACT_EINVAL, "codes, scales and out are required");
+  const void* ps[5] = {a_codes, a_scales, w_codes, w_scales, out};
+  for (const void* q : ps)
+    if (!aligned(q, 16)) return fail(MOEACT_EALIGN, "codes, scales and out must be 16-byte aligned");
+  if (ldo < N) return fail(MOEACT_EINVAL, "output row stride (%lld) smaller than %s", (long long)ldo, nn);
+  if (ldo % (out_dtype == MOEACT_OUT_FP32 ? 4 : 8) != 0)
+    return fail(MOEACT_EALIGN, "output rows must be 16-byte aligned");
+  if (ldo > (((int64_t)1) << 40) || M * ldo > (((int64_t)1) << 60)) return fail(MOEACT_ERANGE, "out extent too large");
+  if ((ceil_div(M, 128) + E) * ceil_div(N, 128) > INT32_MAX)
+    return fail(MOEACT_ERANGE, "more than 2^31 - 1 tiles of the output");
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  int dev;
+  if ((st = ensure_ready(cs, &dev))) return st;
+  GroupedGemmParams p{};
+  p.row_offs = ro;
+  p.M = M;
+  p.E = E;
+  p.K = (int)K;
+  p.N = (int)N;
+  p.a_scales = static_cast<const uint8_t*>(a_scales);
+  p.b_scales = static_cast<const uint8_t*>(w_scales);
+  p.a_tiled = a_layout == MOEACT_SCALES_GEMM;
+  p.b_tiled = w_layout == MOEACT_SCALES_GEMM;
+  p.out = out;
+  p.ldo = ldo;
+  p.out32 = out_dtype == MOEACT_OUT_FP32;
+  p.status = status;
+  p.noop = noop;
+  p.err = g_err_ptr[dev];
+  const bool pair = gemm_pair(ceil_div(M, 256), ceil_div(N, 256), M / E, dev);
+  const int64_t row_bytes = op == kGemmFwd4 ? K / 2 : K;
+  CUtensorMap ta, tb;
+  if ((st = make_code_map(&ta, a_codes, row_bytes, M, pair ? kGemmBoxRows : kGemmShortBoxRows)))
+    return st;
+  if (dgrad) st = make_code_map(&tb, w_codes, N, wrows, kGemmShortBoxRows);
+  else st = make_code_map(&tb, w_codes, row_bytes, wrows, kGemmBoxRows);
+  if (st) return st;
+  const cudaError_t e = grouped_gemm_launch(op, pair, p, ta, tb, g_sms[dev], cs);
+  if (e != cudaSuccess) return cuda_fail(e, "grouped product launch");
+  return MOEACT_OK;
+}
+
 }  // namespace
+
+cudaError_t grouped_gemm_prepare() {
+  cudaError_t e = grouped_gemm_prepare_fwd();
+  if (e == cudaSuccess) e = grouped_gemm_prepare_dgrad();
+  if (e == cudaSuccess) e = grouped_gemm_prepare_wgrad();
+  if (e == cudaSuccess) e = grouped_gemm_prepare_fwd4();
+  return e;
+}
+
+cudaError_t grouped_gemm_launch(int op, bool pair, const GroupedGemmParams& p,
+                                const CUtensorMap& tm_a, const CUtensorMap& tm_b, int n_sms,
+                                cudaStream_t stream) {
+  switch (op) {
+    case kGemmFwd: return grouped_gemm_launch_fwd(pair, p, tm_a, tm_b, n_sms, stream);
+    case kGemmDgrad: return grouped_gemm_launch_dgrad(pair, p, tm_a, tm_b, n_sms, stream);
+    case kGemmWgrad: return grouped_gemm_launch_wgrad(pair, p, tm_a, tm_b, n_sms, stream);
+    default: return grouped_gemm_launch_fwd4(pair, p, tm_a, tm_b, n_sms, stream);
+  }
+}
+
 }  // namespace moeact
 
 using namespace moeact;
@@ -903,6 +1087,129 @@ moeact_status grouped_scaled_swiglu_mxfp8_fc2(const void* x, int64_t ldx, const 
   const int64_t grid = ceil_div(M, 128) + num_groups + g_sms[dev];
   const cudaError_t e = fc2_launch(p, tx, staged_rounding, (unsigned)grid, cs);
   if (e != cudaSuccess) return cuda_fail(e, "fused FC2 launch");
+  return MOEACT_OK;
+}
+
+// ---------------------------------------------------------------- plain quantizers
+moeact_status mxfp8_quantize(const void* x, int64_t ldx, int64_t M, int64_t N, int dirs,
+                             moeact_mx_out out, void* stream) {
+  return fwd_common(plain(kPlain), x, ldx, nullptr, M, N, dirs, nullptr, nullptr, 0, nullptr, out,
+                    stream, false);
+}
+
+moeact_status grouped_mxfp8_quantize(const void* x, int64_t ldx, int64_t M, int64_t N, int dirs,
+                                     const int64_t* row_offs, const int64_t* colblk_offs,
+                                     int32_t num_groups, int32_t* status, moeact_mx_out out,
+                                     void* stream) {
+  return fwd_common(plain(kPlain), x, ldx, nullptr, M, N, dirs, row_offs, colblk_offs, num_groups,
+                    status, out, stream, true);
+}
+
+moeact_status mxfp4_quantize(const void* x, int64_t ldx, int64_t M, int64_t N, void* codes,
+                             void* scales, int32_t scale_layout, const int32_t* noop_flag,
+                             void* stream) {
+  return mxfp4_common(x, ldx, M, N, codes, scales, scale_layout, noop_flag, stream, false);
+}
+
+moeact_status mxfp4_dequantize(const void* codes, const void* scales, int32_t scale_layout,
+                               int64_t M, int64_t N, void* out, int64_t ldo,
+                               const int32_t* noop_flag, void* stream) {
+  return mxfp4_common(out, ldo, M, N, const_cast<void*>(codes), const_cast<void*>(scales),
+                      scale_layout, noop_flag, stream, true);
+}
+
+// ---------------------------------------------------------------- grouped products
+moeact_status grouped_mxfp8_gemm(const void* a_codes, const void* a_scales,
+                                 int32_t a_scale_layout, int64_t M, int64_t K,
+                                 const int64_t* row_offs, int32_t num_groups, int32_t* status,
+                                 const void* w_codes, const void* w_scales,
+                                 int32_t w_scale_layout, int64_t H, void* out, int64_t ldo,
+                                 int32_t out_dtype, const int32_t* noop_flag, void* stream) {
+  return gemm_rows(kGemmFwd, a_codes, a_scales, a_scale_layout, M, K, row_offs, num_groups, status,
+                   w_codes, w_scales, w_scale_layout, H, out, ldo, out_dtype, noop_flag, stream);
+}
+
+moeact_status grouped_mxfp8_dgrad(const void* dy_codes, const void* dy_scales,
+                                  int32_t dy_scale_layout, int64_t M, int64_t H,
+                                  const int64_t* row_offs, int32_t num_groups, int32_t* status,
+                                  const void* w_codes, const void* w_scales,
+                                  int32_t w_scale_layout, int64_t K, void* dx, int64_t lddx,
+                                  int32_t out_dtype, const int32_t* noop_flag, void* stream) {
+  return gemm_rows(kGemmDgrad, dy_codes, dy_scales, dy_scale_layout, M, H, row_offs, num_groups,
+                   status, w_codes, w_scales, w_scale_layout, K, dx, lddx, out_dtype, noop_flag,
+                   stream);
+}
+
+moeact_status grouped_mxfp4_gemm(const void* a_codes, const void* a_scales,
+                                 int32_t a_scale_layout, int64_t M, int64_t K,
+                                 const int64_t* row_offs, int32_t num_groups, int32_t* status,
+                                 const void* w_codes, const void* w_scales,
+                                 int32_t w_scale_layout, int64_t H, void* out, int64_t ldo,
+                                 int32_t out_dtype, const int32_t* noop_flag, void* stream) {
+  return gemm_rows(kGemmFwd4, a_codes, a_scales, a_scale_layout, M, K, row_offs, num_groups,
+                   status, w_codes, w_scales, w_scale_layout, H, out, ldo, out_dtype, noop_flag,
+                   stream);
+}
+
+moeact_status grouped_mxfp8_wgrad(const void* dy_codes, const void* dy_scales,
+                                  const void* x_codes, const void* x_scales,
+                                  int64_t scale_rows, int32_t scale_layout, int64_t M, int64_t H,
+                                  int64_t K,
+                                  const int64_t* row_offs, const int64_t* colblk_offs,
+                                  int32_t num_groups, int32_t* status, void* dw,
+                                  int32_t out_dtype, int accumulate, const int32_t* noop_flag,
+                                  void* stream) {
+  t_err[0] = 0;
+  moeact_status st = check_gemm_common(M, row_offs, num_groups, status, out_dtype, noop_flag);
+  if (st) return st;
+  // M == 0 has no codes to point at; the gradients are zero all the same
+  if (!dw || !colblk_offs || (M > 0 && (!dy_codes || !dy_scales || !x_codes || !x_scales)))
+    return fail(MOEACT_EINVAL, "codes, scales, colblk_offs and dw are required");
+  if ((st = check_width(H, "H")) || (st = check_width(K, "K"))) return st;
+  if ((st = check_scale_layout(scale_layout, "scale_layout", M, H))) return st;
+  if ((st = check_scale_layout(scale_layout, "scale_layout", M, K))) return st;
+  if (scale_rows < ceil_div(M, 32))
+    return fail(MOEACT_EINVAL, "scale_rows (%lld) below M / 32", (long long)scale_rows);
+  if (accumulate != 0 && accumulate != 1) return fail(MOEACT_EINVAL, "accumulate must be 0 or 1");
+  if (accumulate && out_dtype != MOEACT_OUT_FP32)
+    return fail(MOEACT_EINVAL, "accumulate needs an fp32 dw");
+  const void* ps[5] = {dy_codes, dy_scales, x_codes, x_scales, dw};
+  for (const void* q : ps)
+    if (!aligned(q, 16)) return fail(MOEACT_EALIGN, "codes, scales and dw must be 16-byte aligned");
+  if (!aligned(colblk_offs, 8)) return fail(MOEACT_EALIGN, "colblk_offs must be 8-byte aligned");
+  if ((int64_t)num_groups * ceil_div(H, 128) * ceil_div(K, 128) > INT32_MAX)
+    return fail(MOEACT_ERANGE, "more than 2^31 - 1 tiles of dw");
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  int dev;
+  if ((st = ensure_ready(cs, &dev))) return st;
+  GroupedGemmParams p{};
+  p.row_offs = row_offs;
+  p.cb_offs = colblk_offs;
+  p.cb_rows = scale_rows;
+  p.M = M;
+  p.E = num_groups;
+  p.R = (int)H;
+  p.N = (int)K;
+  p.a_codes = static_cast<const uint8_t*>(dy_codes);
+  p.b_codes = static_cast<const uint8_t*>(x_codes);
+  p.a_scales = static_cast<const uint8_t*>(dy_scales);
+  p.b_scales = static_cast<const uint8_t*>(x_scales);
+  p.a_tiled = p.b_tiled = scale_layout == MOEACT_SCALES_GEMM;
+  p.out = dw;
+  p.ldo = K;
+  p.out32 = out_dtype == MOEACT_OUT_FP32;
+  p.accumulate = accumulate;
+  p.status = status;
+  p.noop = noop_flag;
+  p.err = g_err_ptr[dev];
+  CUtensorMap ta{}, tb{};
+  if (M > 0) {
+    if ((st = make_code_map(&ta, dy_codes, H, M, kGemmShortBoxRows))) return st;
+    if ((st = make_code_map(&tb, x_codes, K, M, kGemmShortBoxRows))) return st;
+  }
+  const bool pair = gemm_pair(num_groups * ceil_div(H, 256), ceil_div(K, 256), H, dev);
+  const cudaError_t e = grouped_gemm_launch(kGemmWgrad, pair, p, ta, tb, g_sms[dev], cs);
+  if (e != cudaSuccess) return cuda_fail(e, "grouped product launch");
   return MOEACT_OK;
 }
 

@@ -1,0 +1,70 @@
+// The grouped block-scaled products (kern_grouped_gemm_*.cu): the host side's
+// view (parameters, tensor-map boxes, launchers).
+//
+// For the rows of each expert e (a group of consecutive rows, any count):
+//   forward   out[i, n]  = sum_k A[i, k] W_e[n, k]
+//   dgrad     out[i, n]  = sum_k A[i, k] W_e[k, n]      (A the output gradient)
+//   wgrad     dW_e[m, n] = sum_i A[i, m] B[i, n]        (i over the expert's rows)
+// with A, B and W block-scaled (E8M0 scales of 32 values along the summed
+// index; E4M3 codes, or E2M1 codes in the forward).
+#pragma once
+
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace moeact {
+
+enum GemmOp : int { kGemmFwd = 0, kGemmDgrad = 1, kGemmWgrad = 2, kGemmFwd4 = 3 };
+
+struct GroupedGemmParams {
+  const int64_t* row_offs;    // [E + 1]
+  const int64_t* cb_offs;     // [E + 1], wgrad only: first block row of each group's scales
+  int64_t cb_rows;            // wgrad: rows that the scale arrays hold
+  int64_t M;                  // rows of all groups
+  int E;
+  int K;                      // forward, dgrad: length of the summed index (multiple of 32)
+  int R;                      // wgrad: rows of dW_e (A's columns)
+  int N;                      // output columns
+  const uint8_t* a_codes;     // wgrad only: row tails are read with plain loads
+  const uint8_t* b_codes;
+  const uint8_t* a_scales;
+  const uint8_t* b_scales;
+  int a_tiled, b_tiled;       // scale layouts: 0 row-major, 1 tiles of 128 x 4
+  void* out;
+  int64_t ldo;                // output row stride in elements
+  int out32;                  // 1: fp32, 0: bf16
+  int accumulate;             // 1: add to what out holds (fp32)
+  int32_t* status;
+  const int32_t* noop;        // nullable
+  uint32_t* err;              // device error word
+};
+
+constexpr int kGemmThreads = 320;   // 4 epilogue, 4 scale, a TMA and an MMA warp
+// Rows of a tensor-map box: 128 (an SM's share of an operand tile), except 32
+// where fewer rows may be wanted: the A rows of the one-SM kernels, whose
+// groups can be short, and operands stored with the summed index outermost,
+// whose last stage can be short.
+constexpr int kGemmBoxRows = 128, kGemmShortBoxRows = 32;
+
+// Sets the kernels' shared-memory limits (once per device).
+cudaError_t grouped_gemm_prepare();
+// pair: 256 x 256 tiles on SM pairs, else 128 x 128 tiles on single SMs.
+cudaError_t grouped_gemm_launch(int op, bool pair, const GroupedGemmParams& p,
+                                const CUtensorMap& tm_a, const CUtensorMap& tm_b, int n_sms,
+                                cudaStream_t stream);
+
+// One translation unit per operator.
+#define MOEACT_GEMM_UNIT(name)                                                                \
+  cudaError_t grouped_gemm_prepare_##name();                                                  \
+  cudaError_t grouped_gemm_launch_##name(bool pair, const GroupedGemmParams& p,               \
+                                         const CUtensorMap& tm_a, const CUtensorMap& tm_b,    \
+                                         int n_sms, cudaStream_t stream);
+MOEACT_GEMM_UNIT(fwd)
+MOEACT_GEMM_UNIT(dgrad)
+MOEACT_GEMM_UNIT(wgrad)
+MOEACT_GEMM_UNIT(fwd4)
+#undef MOEACT_GEMM_UNIT
+
+}  // namespace moeact

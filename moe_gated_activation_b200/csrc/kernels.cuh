@@ -39,7 +39,9 @@
 
 namespace moeact {
 
-enum Act : int { kSwiGLU = 0, kSReLU = 1, kClamped = 2 };   // kClamped: ClampedSwiGLU
+// kClamped: ClampedSwiGLU; kPlain: no activation and no row scale (the plain
+// quantizers: forward kernels only)
+enum Act : int { kSwiGLU = 0, kSReLU = 1, kClamped = 2, kPlain = 3 };
 constexpr int kRow = 1;
 constexpr int kCol = 2;
 // Kernel template flag carried in the DIRS bits: scales in the GEMM-ready
@@ -107,7 +109,7 @@ constexpr int kRowBytes = kTileCols * 2;                   // 256 B of a bf16 ti
 // warp, chosen so that rings + sigmoid table fit the 227 KiB of shared memory.
 template <int ACT, bool BWD>
 struct Cfg {
-  static constexpr bool kSig = ACT != kSReLU;   // gated: sigmoid table, gate + up
+  static constexpr bool kSig = ACT != kSReLU && ACT != kPlain;   // gated: sigmoid table, gate + up
   // the table first in shared memory, looked up by 16-bit addresses
   // (sigma_pair_s): the gated forwards, where it measured faster
   static constexpr bool kSigFront = !BWD && (ACT == kSwiGLU || ACT == kClamped);
@@ -620,10 +622,13 @@ __device__ __forceinline__ void fwd_tile(const Params& p, const Smem& m, Ring<OP
     for (int i = 0; i < 16; ++i) {
       const int r = 16 * h + i;
       const uint2 G = *reinterpret_cast<const uint2*>(sm + i * kRowBytes);
-      const float sr = __shfl_sync(kFull, sv, r);
-      const float2 s2 = make_float2(sr, sr);
+      float2 s2 = make_float2(1.0f, 1.0f);
+      if (ACT != kPlain) s2.x = s2.y = __shfl_sync(kFull, sv, r);
       float2 h01, h23;
-      if (ACT == kClamped) {
+      if (ACT == kPlain) {
+        h01 = bf16x2_to_f2(G.x);
+        h23 = bf16x2_to_f2(G.y);
+      } else if (ACT == kClamped) {
         const uint2 U = *reinterpret_cast<const uint2*>(sm + kOpHalfBytes + i * kRowBytes);
         float2 sg01, sg23;
         sigma_pair_s(m.sig_key, G.x, sg01.x, sg01.y);
@@ -667,7 +672,8 @@ __device__ __forceinline__ void fwd_tile(const Params& p, const Smem& m, Ring<OP
         h01 = mul2(make_float2(r0, r1), make_float2(r0, r1));
         h23 = mul2(make_float2(r2, r3), make_float2(r2, r3));
       }
-      const float2 y01 = mul2(h01, s2), y23 = mul2(h23, s2);
+      const float2 y01 = ACT == kPlain ? h01 : mul2(h01, s2);
+      const float2 y23 = ACT == kPlain ? h23 : mul2(h23, s2);
       const bool live = FULL || r < nrows;
       Y[r][0] = live ? y01.x : 0.0f;
       Y[r][1] = live ? y01.y : 0.0f;
@@ -808,7 +814,7 @@ __global__ void __launch_bounds__(Cfg<ACT, false>::kThreads, 1)
   if (count > 0) {
     cur.init(first, stride, p.n_tiles);
     slab_rows<GROUPED>(p, m, cur.slab, row0, nrows);
-    sv = lane < nrows ? __ldg(p.s + row0 + lane) : 0.0f;
+    if (ACT != kPlain) sv = lane < nrows ? __ldg(p.s + row0 + lane) : 0.0f;
   }
   bool ok = true;
   for (int j = 0; j < count; ++j) {
@@ -819,7 +825,7 @@ __global__ void __launch_bounds__(Cfg<ACT, false>::kThreads, 1)
     float svn = 0.0f;
     if (j + 1 < count) {
       slab_rows<GROUPED>(p, m, nx.slab, row0n, nrowsn);
-      svn = lane < nrowsn ? __ldg(p.s + row0n + lane) : 0.0f;
+      if (ACT != kPlain) svn = lane < nrowsn ? __ldg(p.s + row0n + lane) : 0.0f;
     }
     const bool full = nrows == 32 && (cur.tile + 1) * kTileCols <= p.N;
     // (ClampedSwiGLU with a bf16 limit: the packed-clamp form of the tile)

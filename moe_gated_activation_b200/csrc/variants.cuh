@@ -91,6 +91,8 @@ void fill_bwd_srelu_dense(BwdVariant* t);
 void fill_bwd_srelu_grouped(BwdVariant* t);
 void fill_fwd_clamped_dense(FwdVariant* t);
 void fill_fwd_clamped_grouped(FwdVariant* t);
+void fill_fwd_plain_dense(FwdVariant* t);
+void fill_fwd_plain_grouped(FwdVariant* t);
 void fill_bwd_clamped_dense(BwdVariant* t);
 void fill_bwd_clamped_grouped(BwdVariant* t);
 

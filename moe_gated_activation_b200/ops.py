@@ -35,6 +35,11 @@ class MXFP8(NamedTuple):
     col_scales: torch.Tensor
 
 
+class MXFP4(NamedTuple):
+    codes: torch.Tensor           # uint8 [M, W/2], column 2j in the low half of byte j
+    scales: torch.Tensor          # uint8 E8M0 [M, W/32]
+
+
 class Backward(NamedTuple):
     mx: MXFP8                     # MXFP8 of dX ("grouped_dy")
     dx: Optional[torch.Tensor]    # bf16 [M, W] ("dense_dy")
@@ -512,4 +517,271 @@ def grouped_scaled_swiglu_mxfp8_fc2(x, s, row_offs, w_codes, w_scales, *, status
     _capi.call("grouped_scaled_swiglu_mxfp8_fc2", _ptr(x), ldx, _ptr(s), M, N,
                int(bool(staged_rounding)), _ptr(row_offs), E, _ptr(status), _ptr(w_codes),
                _ptr(w_scales), H, _ptr(out), ldo, _ptr(noop_flag), _stream(dev))
+    return out, status
+
+
+# ------------------------------------------------------------------ plain quantizers
+def _call_on(dev, name, *args):
+    """Calls the library with `dev` current (the tensors' device may be another
+    than the current one), on that device's current stream."""
+    stream = ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(dev.index))
+    if torch.cuda.current_device() == dev.index:
+        _capi.call(name, *args, stream)
+    else:
+        with torch.cuda.device(dev):
+            _capi.call(name, *args, stream)
+
+
+def _layout(gemm_scales):
+    return _capi.SCALES_GEMM if gemm_scales else _capi.SCALES_ROWMAJOR
+
+
+def _flag(noop_flag, dev):
+    if noop_flag is None:
+        return None
+    if noop_flag.dtype != torch.int32 or noop_flag.device != dev or noop_flag.numel() < 1:
+        raise ValueError(f"noop_flag must be an int32 tensor on {dev}")
+    return noop_flag.data_ptr()
+
+
+def _offsets(t, name, E, dev):
+    if t.dtype != torch.int64 or t.dim() != 1 or t.device != dev or not t.is_contiguous() or \
+            (E is not None and t.shape[0] != E + 1) or t.shape[0] < 2:
+        n = "E + 1" if E is None else E + 1
+        raise ValueError(f"{name} must be a contiguous int64 vector of {n} offsets on {dev}")
+    return t.data_ptr()
+
+
+def _status(status, dev):
+    if status is None:
+        return torch.empty(1, dtype=torch.int32, device=dev)
+    if status.dtype != torch.int32 or status.device != dev or status.numel() < 1:
+        raise ValueError(f"status must be an int32 tensor on {dev}")
+    return status
+
+
+def _row_stride(t):
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _quantize8(x, rowwise, colwise, gemm_scales, noop_flag, out, grouped):
+    _check_rows(x, "x", torch.bfloat16, 0)
+    M, N = x.shape
+    dev = x.device
+    dirs = _dirs(rowwise, colwise)
+    if dirs == 0:
+        raise ValueError("at least one of rowwise / colwise is required")
+    col_rows, view = (M + 31) // 32, None
+    if grouped is not None:
+        row_offs, colblk_offs, status, view = grouped
+        E = row_offs.shape[0] - 1
+        ro, cb = _offsets(row_offs, "row_offs", None, dev), _offsets(colblk_offs, "colblk_offs", E, dev)
+        col_rows += E
+    take = _alloc_mx(M, N, dirs, dev, col_rows) if out is None else \
+        _take_mx(out, M, N, dirs, dev, col_rows)
+    _flag(noop_flag, dev)
+    if M == 0:
+        if grouped is not None:
+            status.zero_()
+        return _mx_result(*take, view)
+    mx = _mx_struct(*take, dirs, gemm_scales, noop_flag)
+    if grouped is None:
+        _call_on(dev, "mxfp8_quantize", x.data_ptr(), _row_stride(x), M, N, dirs, mx)
+    else:
+        _call_on(dev, "grouped_mxfp8_quantize", x.data_ptr(), _row_stride(x), M, N, dirs, ro, cb, E,
+                 status.data_ptr(), mx)
+    return _mx_result(*take, view)
+
+
+def mxfp8_quantize(x, *, rowwise=True, colwise=True, gemm_scales=False, noop_flag=None, out=None):
+    """MXFP8 of the bf16 rows x [M, N] (N a multiple of 32): the numerics,
+    layouts and options of the scaled forwards, with no activation and no row
+    scale.  A weight [E, H, K] is quantized as x = w.view(E * H, K)."""
+    return _quantize8(x, rowwise, colwise, gemm_scales, noop_flag, out, None)
+
+
+def grouped_mxfp8_quantize(x, row_offs, colblk_offs, *, rowwise=True, colwise=True, status=None,
+                           col_scale_rows=None, gemm_scales=False, noop_flag=None, out=None):
+    """Grouped mxfp8_quantize: colwise blocks stay inside each expert's rows.
+    Returns (MXFP8, status); offsets, status and col_scale_rows as for the
+    grouped forwards."""
+    status = _status(status, x.device)
+    return _quantize8(x, rowwise, colwise, gemm_scales, noop_flag, out,
+                      (row_offs, colblk_offs, status, col_scale_rows)), status
+
+
+def _u8(t, name, shape, dev):
+    """The pointer of a contiguous uint8 (or E4M3) tensor of this shape."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dtype != torch.uint8 and t.dtype != torch.float8_e4m3fn:
+        raise TypeError(f"{name} must be uint8 or float8_e4m3fn, got {t.dtype}")
+    if t.device != dev or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor on {dev}, got "
+                         f"{list(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def mxfp4_quantize(x, *, gemm_scales=False, noop_flag=None, out=None):
+    """MXFP4 (E2M1 codes, E8M0 RCEIL scales) of the bf16 rows x [M, N] in 1 x
+    32 blocks, N a multiple of 32.  out: an MXFP4 of the caller's buffers.
+    gemm_scales: scales in the GEMM-ready tiled layout (M and N multiples of
+    128)."""
+    _check_rows(x, "x", torch.bfloat16, 0)
+    M, N = x.shape
+    dev = x.device
+    if N % 32 or N == 0:
+        raise ValueError(f"x must have a positive multiple of 32 columns, got {N}")
+    if out is None:
+        out = MXFP4(torch.empty((M, N // 2), dtype=torch.uint8, device=dev),
+                    torch.empty((M, N // 32), dtype=torch.uint8, device=dev))
+        codes, scales = out.codes.data_ptr(), out.scales.data_ptr()
+    else:
+        codes = _u8(out.codes, "out.codes", (M, N // 2), dev)
+        scales = _u8(out.scales, "out.scales", (M, N // 32), dev)
+    flag = _flag(noop_flag, dev)
+    if M:
+        _call_on(dev, "mxfp4_quantize", x.data_ptr(), _row_stride(x), M, N, codes, scales,
+                 _layout(gemm_scales), flag)
+    return out
+
+
+def mxfp4_dequantize(q, *, gemm_scales=False, noop_flag=None, out=None):
+    """The bf16 values [M, N] that an MXFP4 stands for.  out: a caller-owned
+    bf16 [M, N] tensor with unit column stride."""
+    M, N = q.codes.shape[0], 2 * q.codes.shape[1]
+    dev = q.codes.device
+    if not q.codes.is_cuda:
+        raise ValueError("codes must be a CUDA tensor")
+    codes = _u8(q.codes, "codes", (M, N // 2), dev)
+    scales = _u8(q.scales, "scales", (M, N // 32), dev)
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    elif out.dtype != torch.bfloat16 or tuple(out.shape) != (M, N) or out.stride(1) != 1 or \
+            out.device != dev:
+        raise ValueError(f"out must be a bf16 [{M}, {N}] tensor with unit column stride on {dev}")
+    flag = _flag(noop_flag, dev)
+    if M:
+        _call_on(dev, "mxfp4_dequantize", codes, scales, _layout(gemm_scales), M, N,
+                 out.data_ptr(), _row_stride(out), flag)
+    return out
+
+
+# ------------------------------------------------------------------ grouped products
+_OUT = {torch.bfloat16: _capi.OUT_BF16, torch.float32: _capi.OUT_FP32}
+
+
+def _out_dtype(out_dtype, out):
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in _OUT:
+        raise TypeError(f"the output must be bfloat16 or float32, got {out_dtype}")
+    return out_dtype
+
+
+def _product(name, codes, scales, per_byte, w_codes, w_scales, w_inner, row_offs, out_dtype, out,
+             status, a_gemm, w_gemm, noop_flag):
+    """The row products.  w_inner: W's rows hold the summed index (gemm), not
+    the output columns (dgrad)."""
+    if codes is None or scales is None or w_codes is None or w_scales is None:
+        raise ValueError("codes and scales of both operands are required, "
+                         + ("rowwise" if w_inner else "rowwise of dy and colwise of w"))
+    if not codes.is_cuda or codes.dim() != 2:
+        raise ValueError("the rows' codes must be a 2-D CUDA tensor")
+    dev = codes.device
+    M, K = codes.shape[0], codes.shape[1] * per_byte
+    E = row_offs.shape[0] - 1
+    ro = _offsets(row_offs, "row_offs", None, dev)
+    if w_codes.dim() == 3:
+        w_codes, w_scales = w_codes.flatten(0, 1), w_scales.flatten(0, 1)
+    rows, width = w_codes.shape
+    if rows % E or (width * per_byte if w_inner else rows // E) != K:
+        raise ValueError(f"w of shape {list(w_codes.shape)} does not hold {E} matrices for rows of "
+                         f"{K} values")
+    N = rows // E if w_inner else width
+    a, sa = _u8(codes, "codes", (M, K // per_byte), dev), _u8(scales, "scales", (M, K // 32), dev)
+    w = _u8(w_codes, "w codes", (rows, width), dev)
+    sw = _u8(w_scales, "w scales", (rows, K // 32) if w_inner else (rows // 32, width), dev)
+    dt = _out_dtype(out_dtype, out)
+    if out is None:
+        out = torch.empty((M, N), dtype=dt, device=dev)
+    elif out.dim() != 2 or out.shape[0] != M or out.shape[1] != N or out.stride(1) != 1 or \
+            out.device != dev:
+        raise ValueError(f"out must be a [{M}, {N}] tensor with unit column stride on {dev}")
+    status = _status(status, dev)
+    flag = _flag(noop_flag, dev)
+    if M == 0:
+        status.zero_()
+        return out, status
+    _call_on(dev, name, a, sa, _layout(a_gemm), M, K, ro, E, status.data_ptr(), w, sw,
+             _layout(w_gemm), N, out.data_ptr(), _row_stride(out), _OUT[dt], flag)
+    return out, status
+
+
+def grouped_mxfp8_gemm(a, w, row_offs, *, out_dtype=torch.bfloat16, out=None, status=None,
+                       gemm_scales=False, w_gemm_scales=False, noop_flag=None):
+    """out[i] = A[i] W_e^T for every row i of expert e, of MXFP8 operands: a
+    rowwise [M, K] and w, the rowwise MXFP8 of the [E * H, K] weights (or [E,
+    H, K] views).  gemm_scales / w_gemm_scales: their scales are in the
+    GEMM-ready layout.  Returns (out [M, H], status); out: a caller-owned bf16
+    or fp32 tensor with unit column stride."""
+    return _product("grouped_mxfp8_gemm", a.row_codes, a.row_scales, 1, w.row_codes, w.row_scales,
+                    True, row_offs, out_dtype, out, status, gemm_scales, w_gemm_scales, noop_flag)
+
+
+def grouped_mxfp8_dgrad(dy, w, row_offs, *, out_dtype=torch.bfloat16, out=None, status=None,
+                        gemm_scales=False, w_gemm_scales=False, noop_flag=None):
+    """The gradient of grouped_mxfp8_gemm by its rows: dx[i] = dY[i] W_e, with
+    dy rowwise MXFP8 [M, H] and w the colwise MXFP8 of the [E * H, K] weights.
+    Returns (dx [M, K], status)."""
+    return _product("grouped_mxfp8_dgrad", dy.row_codes, dy.row_scales, 1, w.col_codes,
+                    w.col_scales, False, row_offs, out_dtype, out, status, gemm_scales,
+                    w_gemm_scales, noop_flag)
+
+
+def grouped_mxfp4_gemm(a, w, row_offs, *, out_dtype=torch.bfloat16, out=None, status=None,
+                       gemm_scales=False, w_gemm_scales=False, noop_flag=None):
+    """grouped_mxfp8_gemm of MXFP4 operands (mxfp4_quantize): a [M, K], w of
+    the [E * H, K] weights."""
+    return _product("grouped_mxfp4_gemm", a.codes, a.scales, 2, w.codes, w.scales, True, row_offs,
+                    out_dtype, out, status, gemm_scales, w_gemm_scales, noop_flag)
+
+
+def grouped_mxfp8_wgrad(dy, x, row_offs, colblk_offs, *, out_dtype=torch.float32, out=None,
+                        accumulate=False, status=None, gemm_scales=False, noop_flag=None):
+    """The gradient of grouped_mxfp8_gemm by the weights: dW_e = dY_e^T X_e,
+    with dy [M, H] and x [M, K] colwise MXFP8 (grouped calls with these
+    offsets).  Returns (dw [E, H, K], status); experts without rows get zeros.
+    accumulate: add to `out` (fp32) instead of overwriting it."""
+    if dy.col_codes is None or x.col_codes is None or dy.col_scales is None or x.col_scales is None:
+        raise ValueError("colwise codes and scales of dy and x are required")
+    cy, cx = dy.col_codes, x.col_codes
+    if not cy.is_cuda or cy.dim() != 2 or cx.dim() != 2:
+        raise ValueError("dy and x codes must be 2-D CUDA tensors")
+    dev = cy.device
+    (M, H), K = cy.shape, cx.shape[1]
+    E = row_offs.shape[0] - 1
+    ro, cb = _offsets(row_offs, "row_offs", None, dev), _offsets(colblk_offs, "colblk_offs", E, dev)
+    pc, px = _u8(cy, "dy codes", (M, H), dev), _u8(cx, "x codes", (M, K), dev)
+    for t, name, width in ((dy.col_scales, "dy scales", H), (x.col_scales, "x scales", K)):
+        # the exact number of scale rows, sum ceil(m_e / 32), is on the device;
+        # it is at least ceil(M / 32)
+        if t.dim() != 2 or t.shape[0] < (M + 31) // 32:
+            raise ValueError(f"{name} must have the sum of ceil(m_e / 32) rows")
+        _u8(t, name, (t.shape[0], width), dev)
+    rows = min(dy.col_scales.shape[0], x.col_scales.shape[0])
+    dt = _out_dtype(out_dtype, out)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    if accumulate and dt != torch.float32:
+        raise TypeError("accumulate needs a float32 out")
+    if out is None:
+        out = torch.empty((E, H, K), dtype=dt, device=dev)
+    elif tuple(out.shape) != (E, H, K) or not out.is_contiguous() or out.device != dev:
+        raise ValueError(f"out must be a contiguous [{E}, {H}, {K}] tensor on {dev}")
+    status = _status(status, dev)
+    flag = _flag(noop_flag, dev)
+    _call_on(dev, "grouped_mxfp8_wgrad", pc, dy.col_scales.data_ptr(), px, x.col_scales.data_ptr(),
+             rows, _layout(gemm_scales), M, H, K, ro, cb, E, status.data_ptr(), out.data_ptr(),
+             _OUT[dt], int(bool(accumulate)), flag)
     return out, status

@@ -1,0 +1,439 @@
+"""The grouped products of block-scaled operands against plain 64-bit forms.
+
+Tolerance.  A product of two E4M3 (or E2M1) values has at most 8 (4)
+significant bits and its scales are powers of two, so it is exact in fp32; a
+sum of n of them in any order, with at most one unit in the last place (2^-23
+relative) lost at each of the n additions, is off by at most n 2^-23 sum |a w|.
+The one rounding to the output adds half a step of it: 2^-8 (bf16) or 2^-24
+(fp32) of the result.  So |out - ref| <= h |ref| + (1 + h) n 2^-23 sum |a w|.
+"""
+import ctypes
+
+import pytest
+import torch
+
+import moe_gated_activation_b200 as mg
+import products_ref as ref
+from moe_gated_activation_b200 import _capi
+
+pytestmark = pytest.mark.gpu
+
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _codes(g, *shape):
+    """Every finite E4M3 code."""
+    c = torch.randint(0, 254, shape, generator=g, device="cuda", dtype=torch.int32)
+    return (c + (c >= 0x7F)).to(torch.uint8)
+
+
+def _scales(g, *shape):
+    return torch.randint(118, 131, shape, generator=g, device="cuda", dtype=torch.int32).to(torch.uint8)
+
+
+def _bytes(g, *shape):
+    return torch.randint(0, 256, shape, generator=g, device="cuda", dtype=torch.int32).to(torch.uint8)
+
+
+def _offs(splits):
+    o = [0]
+    for m in splits:
+        o.append(o[-1] + m)
+    return o
+
+
+def _dev(offs):
+    return torch.tensor(offs, dtype=torch.int64, device="cuda")
+
+
+def _blocks(splits):
+    return _offs([(m + 31) // 32 for m in splits])
+
+
+def _check(got, want, size, n, what):
+    h = HALF[got.dtype]
+    err = (got.double() - want).abs()
+    lim = h * want.abs() + (1 + h) * n * 2.0 ** -23 * size
+    assert got.shape == want.shape
+    bad = ~(err <= lim)
+    if bad.any():
+        i = bad.nonzero()[0].tolist()
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} outside; first {i}: "
+                             f"{got[tuple(i)].item()} for {want[tuple(i)].item()}")
+
+
+def _rows_case(op, splits, K, H, seed):
+    """(call, reference, sum of magnitudes, length of the sum, output width)
+    of a row product; K: the weights' columns, H: their rows."""
+    g = _gen(seed)
+    offs, E, M = _offs(splits), len(splits), sum(splits)
+    ro = _dev(offs)
+    if op == "gemm4":
+        a, sa = _bytes(g, M, K // 2), _scales(g, M, K // 32)
+        w, sw = _bytes(g, E * H, K // 2), _scales(g, E * H, K // 32)
+        av, wv = ref.values4(a, sa), ref.values4(w, sw).unflatten(0, (E, H)).mT
+        call = lambda **kw: mg.grouped_mxfp4_gemm(mg.MXFP4(a, sa), mg.MXFP4(w, sw), ro, **kw)
+    elif op == "gemm":
+        a, sa = _codes(g, M, K), _scales(g, M, K // 32)
+        w, sw = _codes(g, E * H, K), _scales(g, E * H, K // 32)
+        av, wv = ref.values8(a, sa, 1), ref.values8(w, sw, 1).unflatten(0, (E, H)).mT
+        call = lambda **kw: mg.grouped_mxfp8_gemm(mg.MXFP8(a, None, sa, None),
+                                                  mg.MXFP8(w, None, sw, None), ro, **kw)
+    else:
+        a, sa = _codes(g, M, H), _scales(g, M, H // 32)
+        w, sw = _codes(g, E * H, K), _scales(g, E * H // 32, K)
+        av, wv = ref.values8(a, sa, 1), ref.values8(w, sw, 0).unflatten(0, (E, H))
+        call = lambda **kw: mg.grouped_mxfp8_dgrad(mg.MXFP8(a, None, sa, None),
+                                                   mg.MXFP8(None, w, None, sw), ro, **kw)
+    want = ref.grouped(lambda e, r: av[r] @ wv[e], offs)
+    size = ref.grouped(lambda e, r: av[r].abs() @ wv[e].abs(), offs)
+    return call, want, size, (H if op == "dgrad" else K), want.shape[1], (a, sa, w, sw, ro)
+
+
+RAGGED = [0, 1, 31, 33, 0, 127, 129, 64, 255, 257, 0]
+SHAPES = [
+    ([1], 32, 32),                       # one row, one block
+    ([1], 2048, 1536),                   # one token of a wide expert
+    ([128], 128, 128),                   # one full tile
+    (RAGGED, 96, 160),
+    (RAGGED, 416, 288),
+    ([3, 0, 2, 1], 2080, 544),
+    ([2, 0, 1] * 100, 64, 32),           # 300 groups
+    ([700, 0, 1300, 130], 1056, 2592),   # pairs of SMs
+    ([4000], 288, 1312),
+    ([513] * 9, 32, 1024),
+]
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("i", range(len(SHAPES)))
+@pytest.mark.parametrize("op", ["gemm", "dgrad", "gemm4"])
+def test_row_products(cuda_device, op, i, out_dtype):
+    splits, K, H = SHAPES[i]
+    call, want, size, n, _, _ = _rows_case(op, splits, K, H, 10 + i)
+    out, status = call(out_dtype=out_dtype)
+    assert int(status) == 0
+    _check(out, want, size, n, (op, splits, K, H))
+
+
+def _wgrad_case(splits, H, K, seed):
+    g = _gen(seed)
+    M, offs, cb = sum(splits), _offs(splits), _blocks(splits)
+    dy, x = _codes(g, M, H), _codes(g, M, K)
+    sy, sx = _scales(g, cb[-1], H), _scales(g, cb[-1], K)
+    yv, xv = ref.values8(dy, sy, 0, offs), ref.values8(x, sx, 0, offs)
+    r = [slice(lo, hi) for lo, hi in zip(offs[:-1], offs[1:])]
+    want = torch.stack([yv[s].T @ xv[s] for s in r])
+    size = torch.stack([yv[s].abs().T @ xv[s].abs() for s in r])
+    return dy, x, sy, sx, _dev(offs), _dev(cb), want, size
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("splits,H,K", [
+    ([1], 32, 32), ([31], 128, 128), ([128], 256, 256), (RAGGED, 160, 96), (RAGGED, 288, 416),
+    ([3, 0, 2, 1], 544, 2080), ([2, 0, 1] * 100, 32, 64), ([700, 0, 1301, 130], 2592, 1056),
+    ([0, 0], 64, 64), ([5000], 320, 2560),
+])
+def test_wgrad(cuda_device, splits, H, K, out_dtype):
+    dy, x, sy, sx, ro, cb, want, size = _wgrad_case(splits, H, K, 40)
+    dw, status = mg.grouped_mxfp8_wgrad(mg.MXFP8(None, dy, None, sy), mg.MXFP8(None, x, None, sx),
+                                        ro, cb, out_dtype=out_dtype)
+    assert int(status) == 0
+    _check(dw, want, size, max(splits), (splits, H, K))
+
+
+def test_wgrad_accumulates(cuda_device):
+    splits, H, K = [33, 0, 95], 96, 288
+    dy, x, sy, sx, ro, cb, want, size = _wgrad_case(splits, H, K, 41)
+    a, b = mg.MXFP8(None, dy, None, sy), mg.MXFP8(None, x, None, sx)
+    once, _ = mg.grouped_mxfp8_wgrad(a, b, ro, cb)
+    held = torch.randn(once.shape, generator=_gen(1), device="cuda")
+    out = held.clone()
+    got, _ = mg.grouped_mxfp8_wgrad(a, b, ro, cb, out=out, accumulate=True)
+    assert got.data_ptr() == out.data_ptr()
+    assert torch.equal(out, held + once)         # one fp32 addition
+
+
+@pytest.mark.parametrize("splits", [[128, 0, 256], [1280, 128, 640]])
+def test_tiled_scales(cuda_device, splits):
+    """Scales in the GEMM-ready layout give the row-major ones' bits."""
+    K, H = 384, 2560
+    E = len(splits)
+    for op in ("gemm", "dgrad", "gemm4"):
+        call, want, size, n, _, (a, sa, w, sw, ro) = _rows_case(op, splits, K, H, 3)
+        plain, _ = call()
+        ta = ref.tile_scales(sa)
+        tw = ref.tile_col_scales(sw, [E * H // 32]) if op == "dgrad" else ref.tile_scales(sw)
+        for a_t, w_t in ((True, True), (True, False), (False, True)):
+            s1, s2 = (ta if a_t else sa), (tw if w_t else sw)
+            kw = dict(gemm_scales=a_t, w_gemm_scales=w_t)
+            if op == "gemm4":
+                got, _ = mg.grouped_mxfp4_gemm(mg.MXFP4(a, s1), mg.MXFP4(w, s2), ro, **kw)
+            elif op == "gemm":
+                got, _ = mg.grouped_mxfp8_gemm(mg.MXFP8(a, None, s1, None),
+                                               mg.MXFP8(w, None, s2, None), ro, **kw)
+            else:
+                got, _ = mg.grouped_mxfp8_dgrad(mg.MXFP8(a, None, s1, None),
+                                                mg.MXFP8(None, w, None, s2), ro, **kw)
+            assert torch.equal(got, plain), (op, a_t, w_t)
+    dy, x, sy, sx, ro, cb, want, size = _wgrad_case(splits, H, K, 4)
+    plain, _ = mg.grouped_mxfp8_wgrad(mg.MXFP8(None, dy, None, sy), mg.MXFP8(None, x, None, sx), ro, cb)
+    nb = [m // 32 for m in splits]
+    got, st = mg.grouped_mxfp8_wgrad(mg.MXFP8(None, dy, None, ref.tile_col_scales(sy, nb)),
+                                     mg.MXFP8(None, x, None, ref.tile_col_scales(sx, nb)), ro, cb,
+                                     gemm_scales=True)
+    assert int(st) == 0 and torch.equal(got, plain)
+
+
+def test_tiled_scales_need_whole_groups(cuda_device):
+    dy, x, sy, sx, ro, cb, _, _ = _wgrad_case([64, 64], 128, 128, 4)
+    out = torch.full((2, 128, 128), 7.0, device="cuda")
+    _, st = mg.grouped_mxfp8_wgrad(mg.MXFP8(None, dy, None, sy), mg.MXFP8(None, x, None, sx), ro,
+                                   cb, gemm_scales=True, out=out)
+    assert int(st) == _capi.DEV_UNALIGNED_GROUPS and bool((out == 7).all())
+
+
+@pytest.mark.parametrize("splits,K,H", [([5, 0, 40, 1], 160, 96), ([300, 0, 2000, 130], 288, 2592)])
+def test_nan_stays_in_its_group(cuda_device, splits, K, H):
+    """A group full of NaN (codes and scales) makes no other group's output
+    NaN, whichever tiles its rows share."""
+    bad = 2
+    lo, hi = _offs(splits)[bad:bad + 2]
+    for op in ("gemm", "dgrad", "gemm4"):
+        call, want, size, n, _, (a, sa, w, sw, ro) = _rows_case(op, splits, K, H, 5)
+        a[lo:hi] = 0x7F
+        sa[lo:hi] = 255
+        e = w.shape[0] // len(splits)
+        w[bad * e:(bad + 1) * e] = 0x7F
+        sw.view(len(splits), -1, sw.shape[1])[bad] = 255
+        out, _ = call()
+        assert bool(out[lo:hi].isnan().all())
+        keep = [r for r in range(sum(splits)) if not lo <= r < hi]
+        _check(out[keep], want[keep], size[keep], n, op)
+    dy, x, sy, sx, ro, cb, want, size = _wgrad_case(splits, H, K, 6)
+    b0, b1 = _blocks(splits)[bad:bad + 2]
+    for t, s in ((dy, sy), (x, sx)):
+        t[lo:hi] = 0x7F
+        s[b0:b1] = 255
+    dw, _ = mg.grouped_mxfp8_wgrad(mg.MXFP8(None, dy, None, sy), mg.MXFP8(None, x, None, sx), ro, cb)
+    assert bool(dw[bad].isnan().all())
+    keep = [e for e in range(len(splits)) if e != bad]
+    _check(dw[keep], want[keep], size[keep], max(splits), "wgrad")
+
+
+def test_extreme_scales(cuda_device):
+    """Scales whose product leaves fp32's range overflow to infinity and
+    vanish to zero; 2^-127 times 2^127 is one."""
+    for b, want in ((254, float("inf")), (0, 0.0)):
+        a = torch.full((4, 32), 0x38, dtype=torch.uint8, device="cuda")      # 1.0
+        s = torch.full((4, 1), b, dtype=torch.uint8, device="cuda")
+        w, sw = a.repeat(8, 1), s.repeat(8, 1)
+        ro = _dev([0, 4])
+        out, _ = mg.grouped_mxfp8_gemm(mg.MXFP8(a, None, s, None), mg.MXFP8(w, None, sw, None), ro,
+                                       out_dtype=torch.float32)
+        assert bool((out == want).all()), b
+        out, _ = mg.grouped_mxfp8_gemm(mg.MXFP8(a, None, s, None),
+                                       mg.MXFP8(w, None, 254 - sw, None), ro,
+                                       out_dtype=torch.float32)
+        assert bool((out == 32).all()), b
+
+
+@pytest.mark.parametrize("op", ["gemm", "dgrad", "gemm4"])
+def test_wide_output_and_status(cuda_device, op):
+    """A view of a wider output keeps its other columns; bad offsets and a set
+    no-op flag write nothing."""
+    splits, K, H = [40, 0, 90], 160, 96
+    call, want, size, n, N, case = _rows_case(op, splits, K, H, 7)
+    M = sum(splits)
+    for dt in HALF:
+        wide = torch.full((M, N + 16), 5.0, dtype=dt, device="cuda")
+        out, _ = call(out=wide[:, 8:8 + N])
+        _check(out, want, size, n, op)
+        assert bool((wide[:, :8] == 5).all()) and bool((wide[:, 8 + N:] == 5).all())
+    ro = case[4]
+    good = ro.clone()
+    for bad in ([-1, 40, 40, 130], [0, 50, 40, 130], [0, 40, 40, 129], [0, 40, 200, 130]):
+        ro.copy_(_dev(bad))
+        out = torch.full((M, N), 5.0, dtype=torch.bfloat16, device="cuda")
+        _, st = call(out=out)
+        assert int(st) == _capi.DEV_BAD_OFFSETS and bool((out == 5).all())
+    ro.copy_(good)
+    st = torch.full((1,), 99, dtype=torch.int32, device="cuda")
+    call(out=out, status=st, noop_flag=torch.ones(1, dtype=torch.int32, device="cuda"))
+    assert int(st) == 99 and bool((out == 5).all())
+    call(out=out, status=st, noop_flag=torch.zeros(1, dtype=torch.int32, device="cuda"))
+    assert int(st) == 0
+    _check(out, want, size, n, op)
+
+
+def test_wgrad_status(cuda_device):
+    dy, x, sy, sx, ro, cb, want, size = _wgrad_case([40, 0, 90], 96, 160, 8)
+    a, b = mg.MXFP8(None, dy, None, sy), mg.MXFP8(None, x, None, sx)
+    out = torch.full(want.shape, 5.0, device="cuda")
+    for r, c in (([0, 50, 40, 130], cb), (ro, [0, 2, 2, 4]), (ro, [1, 3, 3, 6]), (ro, [0, 2, 3, 6])):
+        r = r if isinstance(r, torch.Tensor) else _dev(r)
+        c = c if isinstance(c, torch.Tensor) else _dev(c)
+        _, st = mg.grouped_mxfp8_wgrad(a, b, r, c, out=out)
+        assert int(st) == _capi.DEV_BAD_OFFSETS and bool((out == 5).all())
+    # offsets that need more scale rows than there are: 130 single rows
+    one = _dev(list(range(131)))
+    _, st = mg.grouped_mxfp8_wgrad(a, b, one, one)
+    assert int(st) == _capi.DEV_BAD_OFFSETS
+    mg.grouped_mxfp8_wgrad(a, b, ro, cb, out=out,
+                           noop_flag=torch.ones(1, dtype=torch.int32, device="cuda"))
+    assert bool((out == 5).all())
+
+
+def test_no_rows(cuda_device):
+    g = _gen(1)
+    ro = _dev([0, 0, 0])
+    e = torch.empty((0, 64), dtype=torch.uint8, device="cuda")
+    es = torch.empty((0, 2), dtype=torch.uint8, device="cuda")
+    w, sw = _codes(g, 128, 64), _scales(g, 128, 2)
+    out, st = mg.grouped_mxfp8_gemm(mg.MXFP8(e, None, es, None), mg.MXFP8(w, None, sw, None), ro)
+    assert out.shape == (0, 64) and int(st) == 0
+    es = torch.empty((0, 64), dtype=torch.uint8, device="cuda")
+    dw, st = mg.grouped_mxfp8_wgrad(mg.MXFP8(None, e, None, es), mg.MXFP8(None, e, None, es), ro, ro)
+    assert int(st) == 0 and dw.shape == (2, 64, 64) and bool((dw == 0).all())
+
+
+def test_graph_replay_with_new_rows(cuda_device):
+    """A captured product follows the offsets and contents of each replay; two
+    graphs and an eager call on another stream do not disturb one another."""
+    K, H = 288, 2592
+    first, second = [700, 0, 1300, 130], [30, 2000, 99, 1]
+    call, want, size, n, _, (a, sa, w, sw, ro) = _rows_case("gemm", first, K, H, 9)
+    out = torch.empty((2130, H), dtype=torch.bfloat16, device="cuda")
+    dy, x, sy, sx, ro2, cb2, dwant, dsize = _wgrad_case([50, 0, 201], 288, 544, 10)
+    dw = torch.empty(dwant.shape, device="cuda")
+    ya, xa = mg.MXFP8(None, dy, None, sy), mg.MXFP8(None, x, None, sx)
+    call(out=out)
+    mg.grouped_mxfp8_wgrad(ya, xa, ro2, cb2, out=dw)
+    torch.cuda.synchronize()
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1):
+        call(out=out)
+    with torch.cuda.graph(g2):
+        mg.grouped_mxfp8_wgrad(ya, xa, ro2, cb2, out=dw)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for splits in (first, second):
+        offs = _offs(splits)
+        ro.copy_(_dev(offs))
+        av, wv = ref.values8(a, sa, 1), ref.values8(w, sw, 1).unflatten(0, (4, H)).mT
+        want = ref.grouped(lambda e, r: av[r] @ wv[e], offs)
+        size = ref.grouped(lambda e, r: av[r].abs() @ wv[e].abs(), offs)
+        out.zero_()
+        dw.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s1):
+            g1.replay()
+        with torch.cuda.stream(s2):
+            g2.replay()
+            eager, _ = call()
+        torch.cuda.synchronize()
+        _check(out, want, size, n, splits)
+        _check(eager, want, size, n, splits)
+        _check(dw, dwant, dsize, 201, "wgrad")
+
+
+def test_results_repeat(cuda_device):
+    """The same call gives the same bits."""
+    call, *_ = _rows_case("dgrad", [700, 0, 1300, 130], 1056, 2592, 11)
+    a, b = call()[0], call()[0]
+    assert torch.equal(a, b)
+
+
+def _exact_values(g, *shape):
+    """Quarters of at most 15/4: any 32 of them are exact in MXFP8, whichever
+    way the blocks run."""
+    return (torch.randint(-15, 16, shape, generator=g, device="cuda") / 4).bfloat16()
+
+
+@pytest.mark.parametrize("splits,K,H", [([5, 0, 33, 1], 96, 160), ([400, 0, 1900, 130], 288, 2592)])
+def test_gradients_are_the_products_gradients(cuda_device, splits, K, H):
+    """On values that MXFP8 holds exactly: <dOut, A W^T> has the gradients
+    dgrad and wgrad give, by the formula and by differences of the product."""
+    g = _gen(12)
+    E, M, offs = len(splits), sum(splits), _offs(splits)
+    x, w, dy = _exact_values(g, M, K), _exact_values(g, E * H, K), _exact_values(g, M, H)
+    ro, cb, _ = mg.splits_to_offsets(torch.tensor(splits, device="cuda"), M)
+    qx, _ = mg.grouped_mxfp8_quantize(x, ro, cb)
+    qy, _ = mg.grouped_mxfp8_quantize(dy, ro, cb)
+    qw = mg.mxfp8_quantize(w)
+    f32 = dict(out_dtype=torch.float32)
+    out, _ = mg.grouped_mxfp8_gemm(qx, qw, ro, **f32)
+    dx, _ = mg.grouped_mxfp8_dgrad(qy, qw, ro, **f32)
+    dw, _ = mg.grouped_mxfp8_wgrad(qy, qx, ro, cb, **f32)
+    xd, wd, yd = x.double(), w.double().unflatten(0, (E, H)), dy.double()
+    # sums of sixteenths below 2^15: exact in fp32
+    assert torch.equal(out.double(), ref.grouped(lambda e, r: xd[r] @ wd[e].T, offs))
+    assert torch.equal(dx.double(), ref.grouped(lambda e, r: yd[r] @ wd[e], offs))
+    want = torch.stack([yd[lo:hi].T @ xd[lo:hi] for lo, hi in zip(offs[:-1], offs[1:])])
+    assert torch.equal(dw.double(), want)
+    # differences: the product is linear, so a step in one entry moves
+    # <dOut, out> by exactly the step times the gradient
+    row, col = offs[2] + 3, 37
+    x2 = x.clone()
+    x2[row, col] = 1.25 if x[row, col] != 1.25 else -0.5
+    q2, _ = mg.grouped_mxfp8_quantize(x2, ro, cb)
+    out2, _ = mg.grouped_mxfp8_gemm(q2, qw, ro, **f32)
+    step = (x2[row, col] - x[row, col]).double()
+    moved = ((out2.double() - out.double()) * yd).sum()
+    assert moved == step * dx[row, col].double()
+    w2 = w.clone()
+    w2[2 * H + 7, col] = 1.25 if w[2 * H + 7, col] != 1.25 else -0.5
+    out3, _ = mg.grouped_mxfp8_gemm(qx, mg.mxfp8_quantize(w2), ro, **f32)
+    step = (w2[2 * H + 7, col] - w[2 * H + 7, col]).double()
+    assert ((out3.double() - out.double()) * yd).sum() == step * dw[2, 7, col].double()
+
+
+def test_expert_layer_step(cuda_device):
+    """The run of an expert layer's training step: quantize, first product,
+    activation, second product, and back, each product against 64-bit forms of
+    the operands that the step before it wrote."""
+    tokens, hidden, inner = [65, 0, 200, 7], 256, 160
+    E, M, offs = len(tokens), sum(tokens), _offs(tokens)
+    g = _gen(13)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    x, dout, s = rnd(M, hidden), rnd(M, hidden), torch.rand(M, generator=g, device="cuda")
+    w1 = mg.mxfp8_quantize(rnd(E * 2 * inner, hidden) / 16)
+    w2 = mg.mxfp8_quantize(rnd(E * hidden, inner) / 16)
+    ro, cb, _ = mg.splits_to_offsets(torch.tensor(tokens, device="cuda"), M)
+    qx, _ = mg.grouped_mxfp8_quantize(x, ro, cb)
+    h, _ = mg.grouped_mxfp8_gemm(qx, w1, ro)
+    qa, _ = mg.grouped_scaled_swiglu_mxfp8_fwd(h, s, ro, cb)
+    out, _ = mg.grouped_mxfp8_gemm(qa, w2, ro)
+    qd, _ = mg.grouped_mxfp8_quantize(dout, ro, cb)
+    da, _ = mg.grouped_mxfp8_dgrad(qd, w2, ro)
+    dw2, _ = mg.grouped_mxfp8_wgrad(qd, qa, ro, cb)
+    bw, _ = mg.grouped_scaled_swiglu_mxfp8_bwd(da, h, s, ro, cb)
+    dx, _ = mg.grouped_mxfp8_dgrad(bw.mx, w1, ro)
+    dw1, _ = mg.grouped_mxfp8_wgrad(bw.mx, qx, ro, cb)
+
+    def rows(q, w, wdim):
+        a = ref.values8(q.row_codes, q.row_scales, 1)
+        b = (ref.values8(w.row_codes, w.row_scales, 1) if wdim == 1 else
+             ref.values8(w.col_codes, w.col_scales, 0)).unflatten(0, (E, -1))
+        b = b.mT if wdim == 1 else b
+        return [ref.grouped(lambda e, r: f(a[r]) @ f(b[e]), offs) for f in (lambda t: t, torch.abs)]
+
+    def weights(p, q):
+        a, b = (ref.values8(t.col_codes, t.col_scales, 0, offs) for t in (p, q))
+        r = [slice(lo, hi) for lo, hi in zip(offs[:-1], offs[1:])]
+        return [torch.stack([f(a[i]).T @ f(b[i]) for i in r]) for f in (lambda t: t, torch.abs)]
+
+    _check(h, *rows(qx, w1, 1), hidden, "h")
+    _check(out, *rows(qa, w2, 1), inner, "out")
+    _check(da, *rows(qd, w2, 0), hidden, "da")
+    _check(dx, *rows(bw.mx, w1, 0), 2 * inner, "dx")
+    _check(dw2, *weights(qd, qa), 200, "dw2")
+    _check(dw1, *weights(bw.mx, qx), 200, "dw1")
+    err = ctypes.c_uint32(0)
+    _capi.call("moeact_device_error", ctypes.byref(err))
+    assert err.value == 0
