@@ -11,8 +11,9 @@
 // wave share the rows of A and one expert's W in L2).  Roles, per SM:
 //   warps 0-3  epilogue: accumulator -> registers -> rounding -> shared
 //              memory -> whole 128-byte row segments of the output;
-//   warps 4-7  scales: each stage's E8M0 words from global memory straight
-//              into tensor memory (tcgen05.st), from either scale layout;
+//   warps 4-7  scales: E8M0 words from global memory, in either layout, some
+//              chunks ahead into shared memory, and each stage's from there
+//              into tensor memory (tcgen05.st);
 //   warp 8     TMA loads of the code tiles (128 rows x 128 bytes each);
 //   warp 9     tensor-memory allocation; in the pair's first SM the MMAs.
 // One ring of stages carries codes and scales: `full` collects the TMA bytes
@@ -47,7 +48,7 @@ struct GemmCfg {
   static constexpr int kCG = PAIR ? 2 : 1;
   static constexpr int kTM = 128 * kCG;
   static constexpr int kBN = PAIR ? 256 : 128;
-  static constexpr int kStages = PAIR ? 5 : 6;
+  static constexpr int kStages = 5;
   static constexpr int kStageK = kF4 ? 256 : 128;      // summed index per stage
   static constexpr int kMmaK = kF4 ? 64 : 32;
   static constexpr int kWords = kF4 ? 2 : 1;           // scale words per row and stage
@@ -59,7 +60,9 @@ struct GemmCfg {
   static constexpr int kABox = kAmn || !PAIR ? kGemmShortBoxRows : kGemmBoxRows;
   static constexpr int kBBox = kBmn ? kGemmShortBoxRows : kGemmBoxRows;
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kFixed = kStages * kStageBytes + 4 * kEpiWarpBytes + kGemmMisc;
+  static constexpr int kGroups = 1 + kBN / 128;        // 128-row groups of scales (and warps)
+  static constexpr int kSfBytes = 2 * 8 * kGroups * 512;   // two chunks of 8 words
+  static constexpr int kFixed = kStages * kStageBytes + 4 * kEpiWarpBytes + kSfBytes + kGemmMisc;
   static_assert(kAcc1 >= 0 && kAcc1 + kBN <= kSfCol, "tensor-memory columns overlap");
   static_assert(kOverlap % 64 == 0, "the overlap is drained in chunks of 64 columns");
 };
@@ -67,13 +70,15 @@ struct GemmCfg {
 struct GemmSmem {
   unsigned char* stages;
   unsigned char* epi;
+  unsigned char* sf;   // [2][8 words][A's rows, B's rows by 128][512] scale words
   uint64_t* full;      // [kStages] (first SM of a pair) codes and scales are in
   uint64_t* empty;     // [kStages] the stage's MMAs are done
   uint64_t* d_full;    // [2] an accumulator holds a finished tile
   uint64_t* d_empty;   // [2] (first SM) its columns may be overwritten
   int* misc;           // [0] tensor-memory base, [1] abort
   int* scan;           // [10] warp totals
-  int* pre;            // [E + 1] row tiles before each expert
+  int* ro;             // [E + 1] the row offsets (below 2^30)
+  int* pre;            // [E + 1] row tiles before each expert (not wgrad)
 };
 
 __device__ __forceinline__ bool gemm_aborted(const GemmSmem& m) {
@@ -107,8 +112,8 @@ __device__ __forceinline__ GemmTile gemm_tile(const GroupedGemmParams& p, const 
     r.e = mt / ht;
     r.row0 = (mt - r.e * ht) * C::kTM + 128 * rank;
     r.rows = max(0, min(128, p.R - (int)r.row0));
-    r.k0 = p.row_offs[r.e];
-    r.krows = (int)(p.row_offs[r.e + 1] - r.k0);
+    r.k0 = m.ro[r.e];
+    r.krows = m.ro[r.e + 1] - (int)r.k0;
     r.kb = (r.krows + 31) >> 5;
   } else {
     int lo = 0, hi = p.E - 1;   // largest e with pre[e] <= mt (then mt < pre[e + 1])
@@ -117,8 +122,8 @@ __device__ __forceinline__ GemmTile gemm_tile(const GroupedGemmParams& p, const 
       if (m.pre[mid] <= mt) lo = mid; else hi = mid - 1;
     }
     r.e = lo;
-    r.row0 = p.row_offs[lo] + (int64_t)(mt - m.pre[lo]) * C::kTM + 128 * rank;
-    r.rows = (int)max((int64_t)0, min((int64_t)128, p.row_offs[lo + 1] - r.row0));
+    r.row0 = m.ro[lo] + (mt - m.pre[lo]) * C::kTM + 128 * rank;
+    r.rows = max(0, min(128, m.ro[lo + 1] - (int)r.row0));
     r.k0 = 0;
     r.krows = 0;
     r.kb = p.K >> 5;
@@ -127,116 +132,323 @@ __device__ __forceinline__ GemmTile gemm_tile(const GroupedGemmParams& p, const 
 }
 
 // ------------------------------------------------------------ scales
-// The four scale bytes of blocks 4u .. 4u + 3 (u: word index along the summed
-// index) of row r of a [rows, pitch] scale matrix; 0 past its end.
-__device__ __forceinline__ uint32_t row_scale_word(const uint8_t* s, bool tiled, int64_t rows,
-                                                   int pitch, int64_t r, int u) {
-  if (r >= rows || 4 * u >= pitch) return 0u;
-  if (tiled)
-    return __ldg(reinterpret_cast<const uint32_t*>(
-        s + (((r >> 7) * (pitch >> 2) + u) << 9) + ((r & 31) << 4) + (((r >> 5) & 3) << 2)));
-  const uint8_t* a = s + r * pitch + 4 * u;
-  if ((pitch & 3) == 0) return __ldg(reinterpret_cast<const uint32_t*>(a));
-  uint32_t v = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (4 * u + j < pitch) v |= (uint32_t)__ldg(a + j) << (8 * j);
+// A word holds the scales of four consecutive blocks of one row of an operand
+// (rows of the output); a stage needs one word (E4M3) or two (E2M1) per row.
+// A loading warp serves 128 rows of one operand: it keeps kChunk words of each
+// row in registers, two chunks ahead, and writes them to shared memory in
+// pieces of 128 words.
+constexpr int kChunk = 8;
+
+// Loads that stay where they are written: a chunk ahead of their use.
+__device__ __forceinline__ uint32_t ldg32(const uint8_t* a) {
+  uint32_t v;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(a));
   return v;
 }
-// The same for a matrix with the blocks outermost: scale rows b0 .. b0 + nb - 1
-// hold the blocks, `width` columns.  Tiled: the transposed [width, blocks]
-// matrix in tiles, `b0` blocks of its 128-aligned part before this one and
-// tile_cols words in all, starting at byte `base`.
-__device__ __forceinline__ uint32_t col_scale_word(const uint8_t* s, bool tiled, int width,
-                                                   int64_t b0, int nb, int64_t base, int u0,
-                                                   int tile_cols, int c, int u) {
-  if (c >= width || 4 * u >= nb) return 0u;
-  if (tiled)
-    return __ldg(reinterpret_cast<const uint32_t*>(
-        s + base + (((int64_t)(c >> 7) * tile_cols + u0 + u) << 9) + ((c & 31) << 4) +
-        (((c >> 5) & 3) << 2)));
-  const uint8_t* a = s + (b0 + 4 * u) * width + c;
-  uint32_t v = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (4 * u + j < nb) v |= (uint32_t)__ldg(a + (int64_t)j * width) << (8 * j);
+__device__ __forceinline__ uint4 ldg128(const uint8_t* a) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(a));
   return v;
 }
 
+// How a warp fetches: fixed per operand and launch, so that no load meets
+// another path's registers (the loads are unconditional, at addresses clamped
+// into the array: what lies outside is never used, and a load under a
+// condition was waited for where the paths join, a chunk too early).
+enum ScaleMode : int {
+  kTiled = 0,       // 128 x 4 tiles
+  kRows32 = 1,      // row-major, a row's blocks a multiple of 32 bytes
+  kRows16 = 2,      // ... of 16
+  kRows4 = 3,       // ... of 4
+  kRowsAny = 4,     // ... any: aligned words, shifted into place
+  kCols = 5,        // row-major, blocks outermost
+};
+
+// Where a warp's scales of a tile come from.
+struct ScaleSrc {
+  const uint8_t* s;   // the operand's scales
+  int64_t r0;         // rows: first row; columns: first scale row of the group
+  int64_t rows;       // rows: rows that exist
+  int pitch;          // rows: bytes (blocks) of a row; columns: width
+  int c0;             // columns: first column
+  int nb;             // columns: blocks of the summed index
+  int64_t tile0;      // tiled: index of the first 512-byte tile
+  int words;          // words of the summed index
+};
+
 template <typename C>
-__device__ __forceinline__ void load_scale_words(const GroupedGemmParams& p, const GemmTile& t,
-                                                 int u, int q, int lane, uint32_t* w) {
-  if constexpr (C::kAmn) {
-    const int64_t b0 = p.cb_offs[t.e];
-    const int kt = t.krows >> 7;
-    w[0] = col_scale_word(p.a_scales, p.a_tiled, p.R, b0, t.kb, (t.k0 >> 5) * p.R, 0, kt,
-                          (int)t.row0 + 32 * q + lane, u);
-#pragma unroll
-    for (int c = 0; c < C::kSfbCols; ++c)
-      w[1 + c] = col_scale_word(p.b_scales, p.b_tiled, p.N, b0, t.kb, (t.k0 >> 5) * p.N, 0, kt,
-                                t.n0 + 32 * c + lane, u);
+__device__ __forceinline__ ScaleSrc scale_src(const GroupedGemmParams& p, const GemmTile& t,
+                                              int group) {
+  ScaleSrc r;
+  const bool a = group == 0;
+  r.s = a ? p.a_scales : p.b_scales;
+  r.r0 = r.rows = r.tile0 = 0;
+  r.pitch = p.K >> 5;
+  r.c0 = r.nb = 0;
+  if (C::kAmn) {
+    r.r0 = p.cb_offs[t.e];
+    r.pitch = a ? p.R : p.N;
+    r.c0 = a ? (int)t.row0 : t.n0 + 128 * (group - 1);
+    r.nb = t.kb;
+    // the group's [width, blocks] matrix starts at byte k0 / 32 * width
+    r.tile0 = ((t.k0 >> 5) * r.pitch >> 9) +
+              (int64_t)(min(r.c0, r.pitch - 1) >> 7) * (t.krows >> 7);
+  } else if (a) {
+    r.r0 = t.row0;
+    r.rows = p.M;
+  } else if (C::kBmn) {
+    // W quantised as one [E K, N] matrix in blocks of 32 rows
+    r.nb = r.pitch;
+    r.r0 = (int64_t)t.e * r.nb;
+    r.pitch = p.N;
+    r.c0 = t.n0 + 128 * (group - 1);
+    r.tile0 = (int64_t)(min(r.c0, r.pitch - 1) >> 7) * (((int64_t)p.E * r.nb) >> 2) + (r.r0 >> 2);
   } else {
-    const int pitch = p.K >> 5;
-    w[0] = row_scale_word(p.a_scales, p.a_tiled, p.M, pitch, t.row0 + 32 * q + lane, u);
-    if constexpr (C::kBmn) {
-      // W quantised as one [E K, N] matrix in blocks of 32 rows
-      const int64_t b0 = (int64_t)t.e * pitch;
+    r.r0 = (int64_t)t.e * p.N + t.n0 + 128 * (group - 1);
+    r.rows = (int64_t)p.E * p.N;
+  }
+  r.words = (t.kb + 3) >> 2;
+  return r;
+}
+
+// Words u .. u + kChunk - 1 of the warp's 128 rows.  Tiled, and row-major with
+// the summed index inside the rows: w[i][j] is row 32 j + lane's (kRowsAny:
+// the aligned words that hold them, one more per row).  kCols: w[i][j] holds
+// columns c0 + 4 lane .. + 3 of block 4 (u + i) + j.
+template <int MODE, bool OUTER>
+__device__ __forceinline__ void fetch_scales(const ScaleSrc& c, int u, int lane,
+                                             uint32_t (*w)[4]) {
+  const int last = c.words - 1;
+  if constexpr (MODE == kTiled && OUTER) {
 #pragma unroll
-      for (int c = 0; c < C::kSfbCols; ++c)
-        w[1 + c] = col_scale_word(p.b_scales, p.b_tiled, p.N, b0, pitch, 0, (int)(b0 >> 2),
-                                  (int)(((int64_t)p.E * pitch) >> 2), t.n0 + 32 * c + lane, u);
-    } else {
-      const int64_t r0 = (int64_t)t.e * p.N + t.n0 + lane, rows = (int64_t)p.E * p.N;
+    for (int i = 0; i < kChunk; ++i) {
+      const uint4 v = ldg128(c.s + ((c.tile0 + min(u + i, last)) << 9) + 16 * lane);
+      w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+    }
+  } else if constexpr (MODE == kTiled) {
+    // row by row: a group's first row need not be a tile's
 #pragma unroll
-      for (int c = 0; c < C::kSfbCols; ++c)
-        w[1 + c] = row_scale_word(p.b_scales, p.b_tiled, rows, pitch, r0 + 32 * c, u);
+    for (int j = 0; j < 4; ++j) {
+      const int64_t r = min(c.r0 + 32 * j + lane, c.rows - 1);
+      const uint8_t* a = c.s + ((r >> 7) * c.words << 9) + ((r & 31) << 4) + (((r >> 5) & 3) << 2);
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) w[i][j] = ldg32(a + 512 * min(u + i, last));
+    }
+  } else if constexpr (MODE == kCols) {
+    const uint8_t* a = c.s + c.r0 * c.pitch + min(c.c0 + 4 * lane, c.pitch - 4);
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[i][j] = ldg32(a + (int64_t)min(4 * (u + i) + j, c.nb - 1) * c.pitch);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t r = min(c.r0 + 32 * j + lane, c.rows - 1);
+      const uint8_t* a = c.s + r * c.pitch;
+      if constexpr (MODE == kRows32) {
+        // a whole sector in one load: the operand tiles' stream leaves few
+        // request slots
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0][j]), "=r"(w[1][j]), "=r"(w[2][j]), "=r"(w[3][j]),
+                       "=r"(w[4][j]), "=r"(w[5][j]), "=r"(w[6][j]), "=r"(w[7][j])
+                     : "l"(a + 4 * u));
+      } else if constexpr (MODE == kRows16) {
+#pragma unroll
+        for (int i = 0; i < kChunk; i += 4) {
+          const uint4 v = ldg128(a + 4 * min(u + i, last - 3));
+          w[i][j] = v.x, w[i + 1][j] = v.y, w[i + 2][j] = v.z, w[i + 3][j] = v.w;
+        }
+      } else if constexpr (MODE == kRows4) {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) w[i][j] = ldg32(a + 4 * min(u + i, last));
+      } else {
+        // the array starts on a word; a word that holds one of its bytes is
+        // read whole
+        const int64_t end = (c.rows * c.pitch - 1) >> 2, at = (r * c.pitch + 4 * u) >> 2;
+#pragma unroll
+        for (int i = 0; i <= kChunk; ++i) w[i][j] = ldg32(c.s + 4 * min(at + i, end));
+      }
     }
   }
 }
 
-// Warps 4-7 (warp q of them writes lanes 32 q .. 32 q + 31).  Rows of A: lane
-// l of quarter q holds row 32 q + l's word, in all four columns (the MMA
-// reads column q); rows of B: column c, lane l of every quarter holds row
-// 32 c + l's word.  The words of the next stage are loaded before the wait
-// for its slot.
-template <typename C>
-__device__ void gemm_scales(const GroupedGemmParams& p, const GemmSmem& m, uint32_t tbase,
-                            int tiles, int first, int step, int rank) {
-  const int q = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+// A piece of 128 words in shared memory.  A's: row r's word at byte 4 r (each
+// warp reads its own 32).  B's: row 32 j + l's at byte 16 l + 4 j (a lane reads
+// its four).
+template <bool A, int MODE>
+__device__ __forceinline__ void put_words(unsigned char* dst, int lane, const uint32_t* x) {
+  uint32_t w[4] = {x[0], x[1], x[2], x[3]};
+  if constexpr (MODE == kCols) {
+    // four blocks of four columns a lane: a 4 x 4 byte transpose
+    const uint32_t t0 = __byte_perm(x[0], x[1], 0x5140), t1 = __byte_perm(x[2], x[3], 0x5140);
+    const uint32_t t2 = __byte_perm(x[0], x[1], 0x7362), t3 = __byte_perm(x[2], x[3], 0x7362);
+    w[0] = __byte_perm(t0, t1, 0x5410), w[1] = __byte_perm(t0, t1, 0x7632);
+    w[2] = __byte_perm(t2, t3, 0x5410), w[3] = __byte_perm(t2, t3, 0x7632);
+  }
+  if constexpr (A != (MODE == kCols)) {
+    // A, rows 32 j + lane: word 32 j + lane; B, columns 4 lane + j: stored in
+    // the order j = (k + lane / 2) mod 4, so that each store's 32 words fall
+    // into different banks
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (A) {
+        *reinterpret_cast<uint32_t*>(dst + 4 * (32 * k + lane)) = w[k];
+      } else {
+        const int j = (k + (lane >> 1)) & 3;
+        const uint32_t v = j & 2 ? (j & 1 ? w[3] : w[2]) : (j & 1 ? w[1] : w[0]);
+        *reinterpret_cast<uint32_t*>(dst + (4 * (lane & 7) + j) * 16 + (lane >> 3) * 4) = v;
+      }
+    }
+  } else {
+    *reinterpret_cast<uint4*>(dst + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// One of warps 4-7.  LOADER: it fetches a group of 128 rows' words (group 0:
+// A's) two chunks ahead.  All four write every stage's words from shared into
+// tensor memory (tcgen05.st: a tcgen05.cp would take the tensor pipe's time),
+// warp q lanes 32 q .. 32 q + 31: lane l's A word, row 32 q + l's, in column q
+// of four; B column c, row 32 c + l's word.
+template <typename C, bool LOADER, bool OUTER, int MODE, bool A>
+__device__ __forceinline__ void gemm_scales(const GroupedGemmParams& p, const GemmSmem& m,
+                                            uint32_t tbase, int tiles, int first, int step,
+                                            int rank, int group) {
+  const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3;
   const uint32_t dst0 = tbase + ((uint32_t)(32 * q) << 16) + (uint32_t)C::kSfCol;
-  int slot = 0;
+  constexpr int kStagesPerChunk = kChunk / C::kWords;
+  constexpr int kRegs = kChunk + (MODE == kRowsAny ? 1 : 0);
+  constexpr int kChunkBytes = kChunk * C::kGroups * 512;
+  int slot = 0, buf = 0;
   uint32_t phase = 1;   // a fresh barrier's preceding phase counts as complete
-  for (int t = first; t < tiles; t += step) {
-    const GemmTile tile = gemm_tile<C>(p, m, t, rank);
-    const int stages = (tile.kb * 32 + C::kStageK - 1) / C::kStageK;
-    uint32_t w[C::kWords][1 + C::kSfbCols];
-    if (stages > 0)
-      for (int i = 0; i < C::kWords; ++i) load_scale_words<C>(p, tile, i, q, lane, w[i]);
+  // walks the chunks of every tile: chunk `chunk` of tile t
+  struct Walk { int t, chunk, left; };
+  auto next = [&](Walk& k, GemmTile& tile) {   // the next chunk's stages, 0 at the end
+    while (k.left <= 0) {
+      k.t += step;
+      if (k.t >= tiles) return 0;
+      tile = gemm_tile<C>(p, m, k.t, rank);
+      k.left = (tile.kb * 32 + C::kStageK - 1) / C::kStageK;
+      k.chunk = -1;
+    }
+    const int n = min(k.left, kStagesPerChunk);
+    k.left -= n;
+    ++k.chunk;
+    return n;
+  };
+  Walk load = {first - step, 0, 0}, serve = {first - step, 0, 0};
+  ScaleSrc src;
+  GemmTile load_tile, serve_tile;
+  struct Chunk { int word; int64_t r0; };   // what kRowsAny shifts and masks by
+  auto fetch = [&](uint32_t (*w)[4], Chunk& ch) {
+    if constexpr (LOADER) {
+      if (next(load, load_tile) == 0) return;
+      if (load.chunk == 0) src = scale_src<C>(p, load_tile, group);
+      fetch_scales<MODE, OUTER>(src, load.chunk * kChunk, lane, w);
+      ch.word = load.chunk * kChunk;
+      ch.r0 = src.r0;
+    }
+  };
+  auto one = [&](uint32_t (*w)[4], Chunk& ch) {
+    const int stages = next(serve, serve_tile);
+    if (stages == 0) return false;
+    unsigned char* sf = m.sf + buf * kChunkBytes;
+    if constexpr (LOADER) {
+      if constexpr (MODE == kRowsAny) {
+        const int pitch = src.pitch;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int64_t r = min(ch.r0 + 32 * j + lane, src.rows - 1);
+          const int sh = 8 * (int)((r * pitch) & 3);
+#pragma unroll
+          for (int i = 0; i < kChunk; ++i) {
+            w[i][j] = __funnelshift_r(w[i][j], w[i + 1][j], sh);
+            // (bytes past the row's end are another row's: a NaN scale there
+            // would meet the zeros of half an E2M1 step)
+            if (4 * (ch.word + i) + 4 > pitch)
+              w[i][j] &= (1u << (8 * max(0, pitch - 4 * (ch.word + i)))) - 1u;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i)
+        if (i < stages * C::kWords) put_words<A, MODE>(sf + 512 * (C::kGroups * i + group), lane, w[i]);
+      fetch(w, ch);
+    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");   // the chunk is in shared memory
+    bool ok = true;
     for (int s = 0; s < stages; ++s) {
-      if (!__all_sync(kFull, tc::sleep(m.empty + slot, phase)) || gemm_aborted(m)) {
-        gemm_abort(p, m);
-        return;
-      }
-      tc::fence_after();
-      const uint32_t dst = dst0 + slot * C::kSfPitch;
+      ok = ok && __all_sync(kFull, tc::sleep(m.empty + slot, phase));
+      if (ok) {
+        tc::fence_after();
+        const uint32_t dst = dst0 + slot * C::kSfPitch;
 #pragma unroll
-      for (int i = 0; i < C::kWords; ++i) {
-        tc::st4(dst + 4 * i, w[i][0], w[i][0], w[i][0], w[i][0]);
+        for (int i = 0; i < C::kWords; ++i) {
+          const unsigned char* piece = sf + 512 * C::kGroups * (s * C::kWords + i);
+          const uint32_t a = *reinterpret_cast<const uint32_t*>(piece + 4 * (32 * q + lane));
+          tc::st1(dst + 4 * i + q, a);
 #pragma unroll
-        for (int c = 0; c < C::kSfbCols; c += 4)
-          tc::st4(dst + 4 * C::kWords + C::kSfbCols * i + c, w[i][1 + c], w[i][2 + c],
-                  w[i][3 + c], w[i][4 + c]);
+          for (int k = 1; k < C::kGroups; ++k) {
+            const uint4 b = *reinterpret_cast<const uint4*>(piece + 512 * k + 16 * lane);
+            tc::st4(dst + 4 * C::kWords + C::kSfbCols * i + 4 * (k - 1), b.x, b.y, b.z, b.w);
+          }
+        }
+        tc::wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::arrive_cluster(tc::leader_addr(m.full + slot));
       }
-      if (s + 1 < stages)
-        for (int i = 0; i < C::kWords; ++i)
-          load_scale_words<C>(p, tile, (s + 1) * C::kWords + i, q, lane, w[i]);
-      tc::wait_st();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) tc::arrive_cluster(tc::leader_addr(m.full + slot));
       if (++slot == C::kStages) slot = 0, phase ^= 1;
     }
+    if (!ok || gemm_aborted(m)) {
+      ok = false;
+      gemm_abort(p, m);
+    }
+    buf ^= 1;
+    // the four warps leave together after an abort, at a barrier of their own
+    int gone;
+    asm volatile("{ .reg .pred p, r; setp.ne.s32 p, %1, 0; bar.red.or.pred r, 2, 128, p; "
+                 "selp.s32 %0, 1, 0, r; }" : "=r"(gone) : "r"((int)!ok) : "memory");
+    return gone == 0;
+  };
+  uint32_t w0[kRegs][4], w1[kRegs][4];
+  Chunk c0, c1;
+  fetch(w0, c0);
+  fetch(w1, c1);
+  while (one(w0, c0) && one(w1, c1)) {
   }
+}
+
+// The scale warp's role and loads, fixed for the launch.
+template <typename C>
+__device__ __forceinline__ void gemm_scales_any(const GroupedGemmParams& p, const GemmSmem& m,
+                                                uint32_t tbase, int tiles, int first, int step,
+                                                int rank, int group) {
+  const bool tiled = group == 0 ? p.a_tiled : p.b_tiled;
+  const int pitch = p.K >> 5;
+#define MOEACT_SCALES(OUTER, MODE, A) \
+  gemm_scales<C, true, OUTER, MODE, A>(p, m, tbase, tiles, first, step, rank, group)
+#define MOEACT_SCALES_OF(OUTER, A)                             \
+  if constexpr (OUTER) {                                       \
+    if (tiled) MOEACT_SCALES(true, kTiled, A);                 \
+    else MOEACT_SCALES(true, kCols, A);                        \
+  } else {                                                     \
+    if (tiled) MOEACT_SCALES(false, kTiled, A);                \
+    else if ((pitch & 31) == 0) MOEACT_SCALES(false, kRows32, A); \
+    else if ((pitch & 15) == 0) MOEACT_SCALES(false, kRows16, A); \
+    else if ((pitch & 3) == 0) MOEACT_SCALES(false, kRows4, A);   \
+    else MOEACT_SCALES(false, kRowsAny, A);                    \
+  }
+  if (group == 0) {
+    MOEACT_SCALES_OF(C::kAmn, true)
+  } else if (group < C::kGroups) {
+    MOEACT_SCALES_OF(C::kBmn, false)
+  } else {
+    gemm_scales<C, false, false, kRows32, false>(p, m, tbase, tiles, first, step, rank, group);
+  }
+#undef MOEACT_SCALES_OF
+#undef MOEACT_SCALES
 }
 
 // ------------------------------------------------------------ code tiles
@@ -269,7 +481,7 @@ __device__ void gemm_producer(const GroupedGemmParams& p, const GemmSmem& m, con
     const int stages = (tile.kb * 32 + C::kStageK - 1) / C::kStageK;
     const int col_b = tile.n0 + (C::kCG == 2 ? 128 * rank : 0);   // this SM's rows of B
     for (int s = 0; s < stages; ++s) {
-      if (!__all_sync(kFull, tc::spin(m.empty + slot, phase)) || gemm_aborted(m)) {
+      if (!__all_sync(kFull, tc::spin(m.empty + slot, phase))) {
         if (leader) gemm_abort(p, m);
         return;
       }
@@ -350,7 +562,7 @@ __device__ void gemm_mma(const GroupedGemmParams& p, const GemmSmem& m, uint32_t
     tc::fence_after();
     const uint32_t d = tbase + (uint32_t)((n & 1) * C::kAcc1);
     for (int i0 = 0; i0 < mmas; i0 += 4) {
-      if (!__all_sync(kFull, tc::spin(m.full + slot, phase)) || gemm_aborted(m)) {
+      if (!__all_sync(kFull, tc::spin(m.full + slot, phase))) {
         if (leader) gemm_abort(p, m);
         return;
       }
@@ -504,14 +716,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   GemmSmem m;
   m.stages = base;
   m.epi = base + C::kStages * C::kStageBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(m.epi + 4 * kEpiWarpBytes);
+  m.sf = m.epi + 4 * kEpiWarpBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(m.epi + 4 * kEpiWarpBytes + C::kSfBytes);
   m.full = bars;
-  m.empty = bars + C::kStages;
+  m.empty = m.full + C::kStages;
   m.d_full = m.empty + C::kStages;
   m.d_empty = m.d_full + 2;
   m.misc = reinterpret_cast<int*>(bars + 64);
   m.scan = m.misc + 16;
-  m.pre = reinterpret_cast<int*>(reinterpret_cast<unsigned char*>(bars) + kGemmMisc);
+  m.ro = reinterpret_cast<int*>(reinterpret_cast<unsigned char*>(bars) + kGemmMisc);
+  m.pre = m.ro + p.E + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = PAIR ? (int)tc::cluster_rank() : 0;
 
@@ -522,6 +736,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   int local = 0, bad = 0;
   for (int e = e_lo; e < e_hi; ++e) {
     const int64_t r0 = p.row_offs[e], r1 = p.row_offs[e + 1];
+    m.ro[e] = (int)r0;
+    m.ro[e + 1] = (int)r1;   // (the next thread's first writes the same)
     if (r1 < r0 || r0 < 0 || r1 > p.M) bad |= 1;
     else local += (int)((r1 - r0 + C::kTM - 1) / C::kTM);
     if constexpr (C::kWgrad) {
@@ -551,7 +767,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   if constexpr (!C::kWgrad) {
     for (int e = e_lo; e < e_hi; ++e) {
       m.pre[e] = before;
-      before += (int)((p.row_offs[e + 1] - p.row_offs[e] + C::kTM - 1) / C::kTM);
+      before += (m.ro[e + 1] - m.ro[e] + C::kTM - 1) / C::kTM;
     }
     if (tid == 0) m.pre[E] = total;
   } else {
@@ -584,7 +800,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const uint32_t tbase = *reinterpret_cast<volatile uint32_t*>(m.misc);
 
   if (warp < 4) gemm_epilogue<C>(p, m, tbase, tiles, first, step, rank);
-  else if (warp < 8) gemm_scales<C>(p, m, tbase, tiles, first, step, rank);
+  else if (warp < 8) gemm_scales_any<C>(p, m, tbase, tiles, first, step, rank, warp - 4);
   else if (warp == 8) gemm_producer<C>(p, m, &tm_a, &tm_b, tiles, first, step, rank);
   else if (rank == 0) gemm_mma<C>(p, m, tbase, tiles, first, step);
 
@@ -608,7 +824,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 template <int OP, bool PAIR>
 int gemm_smem_bytes(int E) {
   using C = GemmCfg<OP, PAIR>;
-  return 1024 + C::kFixed + (C::kWgrad ? 0 : (E + 1) * 4);
+  return 1024 + C::kFixed + (E + 1) * (C::kWgrad ? 4 : 8);
 }
 
 template <int OP, bool PAIR>

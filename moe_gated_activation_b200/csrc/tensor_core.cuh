@@ -68,7 +68,11 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t adesc, uint64_t bdesc, 
     MOEACT_MMA("tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X");
 #undef MOEACT_MMA
 }
-// Four 32-bit words into four consecutive columns of the warp's 32 lanes.
+// One or four 32-bit words into consecutive columns of the warp's 32 lanes.
+__device__ __forceinline__ void st1(uint32_t taddr, uint32_t v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v)
+               : "memory");
+}
 __device__ __forceinline__ void st4(uint32_t taddr, uint32_t v0, uint32_t v1, uint32_t v2,
                                     uint32_t v3) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};"
@@ -119,11 +123,11 @@ __device__ __forceinline__ uint32_t leader_addr(const void* p) {
 }
 // Arrivals on a barrier of the pair's first SM (bar: its cluster address).
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
 }
 __device__ __forceinline__ void arrive_tx_cluster(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;"
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;"
                ::"r"(bar), "r"(bytes) : "memory");
 }
 // 2-D tile load into this SM's shared memory, completing on the barrier at
@@ -149,14 +153,14 @@ __device__ __forceinline__ void load_2d(void* dst, const void* tmap, int x, int 
 // counts.  Both order what other SMs of the cluster released before arriving.
 __device__ __forceinline__ bool test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, "
+  asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, "
                "[%1], %2; selp.u32 %0, 1, 0, p; }"
                : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
   return ok != 0;
 }
 __device__ __forceinline__ bool test_sleep(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, "
+  asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, "
                "[%1], %2, %3; selp.u32 %0, 1, 0, p; }"
                : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity), "r"(kWaitHintNs) : "memory");
   return ok != 0;
