@@ -341,6 +341,41 @@ moeact_status make_code_map(CUtensorMap* map, const void* base, int64_t bytes, i
   return MOEACT_OK;
 }
 
+// Tensor map of a byte matrix (contiguous rows of `bytes`, a multiple of 16) in
+// plain boxes.
+moeact_status make_byte_map(CUtensorMap* map, const void* base, int64_t bytes, int64_t rows,
+                            int box_bytes, int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)bytes, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)bytes};
+  const cuuint32_t box[2] = {(cuuint32_t)box_bytes, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
+                              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(MOEACT_ECUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return MOEACT_OK;
+}
+
+// Tensor map of a product's output, `groups` matrices of `rows` rows of `cols`
+// values at a stride of `ld` (fp32 or bf16), written in pieces of 32 rows x
+// 128 bytes from swizzled shared memory.
+moeact_status make_out_map(CUtensorMap* map, void* base, int out32, int64_t cols, int64_t rows,
+                           int64_t ld, int64_t groups) {
+  const int es = out32 ? 4 : 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)groups};
+  const cuuint64_t strides[2] = {(cuuint64_t)(ld * es), (cuuint64_t)(rows * ld * es)};
+  const cuuint32_t box[3] = {(cuuint32_t)(kGemmOutBytes / es), (cuuint32_t)kGemmOutRows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = g_encode(
+      map, out32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+      groups > 0 ? 3 : 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(MOEACT_ECUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return MOEACT_OK;
+}
+
 // The backward's map of x: SReLU [rows][N]; gated [rows][2][N] or, with an
 // interleave G, [rows][N/G][2][G].
 moeact_status make_x_map(CUtensorMap* map, int act, const void* x, int64_t N, int ilv,
@@ -779,13 +814,23 @@ moeact_status gemm_rows(int op, const void* a_codes, const void* a_scales, int32
   p.err = g_err_ptr[dev];
   const bool pair = gemm_pair(ceil_div(M, 256), ceil_div(N, 256), M / E, dev);
   const int64_t row_bytes = op == kGemmFwd4 ? K / 2 : K;
-  CUtensorMap ta, tb;
-  if ((st = make_code_map(&ta, a_codes, row_bytes, M, pair ? kGemmBoxRows : kGemmShortBoxRows)))
-    return st;
-  if (dgrad) st = make_code_map(&tb, w_codes, N, wrows, kGemmShortBoxRows);
-  else st = make_code_map(&tb, w_codes, row_bytes, wrows, kGemmBoxRows);
+  const int a_box = pair ? kGemmBoxRows : kGemmShortBoxRows;
+  GemmMaps tm{};
+  if ((st = make_code_map(&tm.a, a_codes, row_bytes, M, a_box))) return st;
+  if (dgrad) st = make_code_map(&tm.b, w_codes, N, wrows, kGemmShortBoxRows);
+  else st = make_code_map(&tm.b, w_codes, row_bytes, wrows, kGemmBoxRows);
   if (st) return st;
-  const cudaError_t e = grouped_gemm_launch(op, pair, p, ta, tb, g_sms[dev], cs);
+  const int64_t pitch = K / 32;
+  if (!p.a_tiled && pitch % 16 == 0 &&
+      (st = make_byte_map(&tm.sa, a_scales, pitch, M, kGemmScaleBytes, a_box)))
+    return st;
+  if (!p.b_tiled) {
+    if (dgrad) st = make_byte_map(&tm.sb, w_scales, N, wrows / 32, 128, 32);
+    else if (pitch % 16 == 0) st = make_byte_map(&tm.sb, w_scales, pitch, wrows, kGemmScaleBytes, 128);
+    if (st) return st;
+  }
+  if ((st = make_out_map(&tm.out, out, p.out32, N, M, ldo, 0))) return st;
+  const cudaError_t e = grouped_gemm_launch(op, pair, p, tm, g_sms[dev], cs);
   if (e != cudaSuccess) return cuda_fail(e, "grouped product launch");
   return MOEACT_OK;
 }
@@ -800,14 +845,13 @@ cudaError_t grouped_gemm_prepare() {
   return e;
 }
 
-cudaError_t grouped_gemm_launch(int op, bool pair, const GroupedGemmParams& p,
-                                const CUtensorMap& tm_a, const CUtensorMap& tm_b, int n_sms,
-                                cudaStream_t stream) {
+cudaError_t grouped_gemm_launch(int op, bool pair, const GroupedGemmParams& p, const GemmMaps& tm,
+                                int n_sms, cudaStream_t stream) {
   switch (op) {
-    case kGemmFwd: return grouped_gemm_launch_fwd(pair, p, tm_a, tm_b, n_sms, stream);
-    case kGemmDgrad: return grouped_gemm_launch_dgrad(pair, p, tm_a, tm_b, n_sms, stream);
-    case kGemmWgrad: return grouped_gemm_launch_wgrad(pair, p, tm_a, tm_b, n_sms, stream);
-    default: return grouped_gemm_launch_fwd4(pair, p, tm_a, tm_b, n_sms, stream);
+    case kGemmFwd: return grouped_gemm_launch_fwd(pair, p, tm, n_sms, stream);
+    case kGemmDgrad: return grouped_gemm_launch_dgrad(pair, p, tm, n_sms, stream);
+    case kGemmWgrad: return grouped_gemm_launch_wgrad(pair, p, tm, n_sms, stream);
+    default: return grouped_gemm_launch_fwd4(pair, p, tm, n_sms, stream);
   }
 }
 
@@ -1202,13 +1246,19 @@ moeact_status grouped_mxfp8_wgrad(const void* dy_codes, const void* dy_scales,
   p.status = status;
   p.noop = noop_flag;
   p.err = g_err_ptr[dev];
-  CUtensorMap ta{}, tb{};
+  GemmMaps tm{};
   if (M > 0) {
-    if ((st = make_code_map(&ta, dy_codes, H, M, kGemmShortBoxRows))) return st;
-    if ((st = make_code_map(&tb, x_codes, K, M, kGemmShortBoxRows))) return st;
+    if ((st = make_code_map(&tm.a, dy_codes, H, M, kGemmShortBoxRows))) return st;
+    if ((st = make_code_map(&tm.b, x_codes, K, M, kGemmShortBoxRows))) return st;
+    if (!p.a_tiled) {
+      const int64_t rows = std::min<int64_t>(scale_rows, ceil_div(M, 32) + num_groups);
+      if ((st = make_byte_map(&tm.sa, dy_scales, H, rows, 128, 32))) return st;
+      if ((st = make_byte_map(&tm.sb, x_scales, K, rows, 128, 32))) return st;
+    }
   }
   const bool pair = gemm_pair(num_groups * ceil_div(H, 256), ceil_div(K, 256), H, dev);
-  const cudaError_t e = grouped_gemm_launch(kGemmWgrad, pair, p, ta, tb, g_sms[dev], cs);
+  if ((st = make_out_map(&tm.out, dw, p.out32, K, H, K, num_groups))) return st;
+  const cudaError_t e = grouped_gemm_launch(kGemmWgrad, pair, p, tm, g_sms[dev], cs);
   if (e != cudaSuccess) return cuda_fail(e, "grouped product launch");
   return MOEACT_OK;
 }

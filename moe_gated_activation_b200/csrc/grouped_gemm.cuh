@@ -47,20 +47,31 @@ constexpr int kGemmThreads = 320;   // 4 epilogue, 4 scale, a TMA and an MMA war
 // groups can be short, and operands stored with the summed index outermost,
 // whose last stage can be short.
 constexpr int kGemmBoxRows = 128, kGemmShortBoxRows = 32;
+// Output: 32 rows of 128 bytes, 128-byte swizzled, of the [M, N] rows or (wgrad)
+// of the [E, R, N] gradients.
+constexpr int kGemmOutRows = 32, kGemmOutBytes = 128;
+
+// Row-major scales: 32 bytes (8 words) of 128 rows (A of the one-SM kernels:
+// of 32), or with the blocks outermost 32 rows of 128 columns.
+constexpr int kGemmScaleBytes = 32;
+
+struct GemmMaps {
+  CUtensorMap a, b;     // code matrices
+  CUtensorMap sa, sb;   // scales, where row-major with steps of 16 bytes
+  CUtensorMap out;
+};
 
 // Sets the kernels' shared-memory limits (once per device).
 cudaError_t grouped_gemm_prepare();
 // pair: 256 x 256 tiles on SM pairs, else 128 x 128 tiles on single SMs.
-cudaError_t grouped_gemm_launch(int op, bool pair, const GroupedGemmParams& p,
-                                const CUtensorMap& tm_a, const CUtensorMap& tm_b, int n_sms,
-                                cudaStream_t stream);
+cudaError_t grouped_gemm_launch(int op, bool pair, const GroupedGemmParams& p, const GemmMaps& tm,
+                                int n_sms, cudaStream_t stream);
 
 // One translation unit per operator.
-#define MOEACT_GEMM_UNIT(name)                                                                \
-  cudaError_t grouped_gemm_prepare_##name();                                                  \
-  cudaError_t grouped_gemm_launch_##name(bool pair, const GroupedGemmParams& p,               \
-                                         const CUtensorMap& tm_a, const CUtensorMap& tm_b,    \
-                                         int n_sms, cudaStream_t stream);
+#define MOEACT_GEMM_UNIT(name)                                                              \
+  cudaError_t grouped_gemm_prepare_##name();                                                \
+  cudaError_t grouped_gemm_launch_##name(bool pair, const GroupedGemmParams& p,             \
+                                         const GemmMaps& tm, int n_sms, cudaStream_t stream);
 MOEACT_GEMM_UNIT(fwd)
 MOEACT_GEMM_UNIT(dgrad)
 MOEACT_GEMM_UNIT(wgrad)

@@ -10,7 +10,7 @@
 // A persistent grid walks the tiles (columns fastest, so that the SMs of a
 // wave share the rows of A and one expert's W in L2).  Roles, per SM:
 //   warps 0-3  epilogue: accumulator -> registers -> rounding -> shared
-//              memory -> whole 128-byte row segments of the output;
+//              memory -> bulk tensor stores of 32 rows x 128 bytes;
 //   warps 4-7  scales: E8M0 words from global memory, in either layout, some
 //              chunks ahead into shared memory, and each stage's from there
 //              into tensor memory (tcgen05.st);
@@ -28,6 +28,8 @@
 // lets what is in flight finish (bounded) and returns.
 #pragma once
 
+#include <type_traits>
+
 #include "grouped_gemm.cuh"
 #include "tensor_core.cuh"
 
@@ -36,8 +38,11 @@ namespace {
 
 constexpr uint32_t kErrGemmWait = 0x40u;
 constexpr int kTileBytes = 16384;         // 128 rows x 128 bytes
-constexpr int kEpiWarpBytes = 4096;       // 32 rows x 128 bytes of output
+constexpr int kPieceBytes = 4096;         // 32 rows x 128 bytes of output
 constexpr int kGemmMisc = 1024;           // barriers and small values
+constexpr int kChunk = 8;                 // scale words of a row fetched together
+constexpr int kRawDepth = 2;              // chunks on their way
+constexpr int kRawBytes = 128 * 36;       // a chunk of 128 rows as it arrives
 
 template <int OP, bool PAIR>
 struct GemmCfg {
@@ -48,21 +53,26 @@ struct GemmCfg {
   static constexpr int kCG = PAIR ? 2 : 1;
   static constexpr int kTM = 128 * kCG;
   static constexpr int kBN = PAIR ? 256 : 128;
-  static constexpr int kStages = 5;
+  static constexpr int kStages = PAIR ? 4 : 5;
   static constexpr int kStageK = kF4 ? 256 : 128;      // summed index per stage
   static constexpr int kMmaK = kF4 ? 64 : 32;
   static constexpr int kWords = kF4 ? 2 : 1;           // scale words per row and stage
   static constexpr int kSfbCols = kBN / 32;
   static constexpr int kSfPitch = kWords * (4 + kSfbCols);
-  static constexpr int kSfCol = 512 - (kStages * kSfPitch + 15) / 16 * 16;
+  static constexpr int kSfCol = 512 - (kStages * kSfPitch + 63) / 64 * 64;
   static constexpr int kAcc1 = PAIR ? kSfCol - kBN : kBN;   // second accumulator's column
   static constexpr int kOverlap = PAIR ? kBN - kAcc1 : 0;
   static constexpr int kABox = kAmn || !PAIR ? kGemmShortBoxRows : kGemmBoxRows;
   static constexpr int kBBox = kBmn ? kGemmShortBoxRows : kGemmBoxRows;
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kGroups = 1 + kBN / 128;        // 128-row groups of scales (and warps)
-  static constexpr int kSfBytes = 2 * 8 * kGroups * 512;   // two chunks of 8 words
-  static constexpr int kFixed = kStages * kStageBytes + 4 * kEpiWarpBytes + kSfBytes + kGemmMisc;
+  static constexpr int kSfBytes = kChunk * kGroups * 512;   // a chunk, ready for tensor memory
+  static constexpr int kRawGroupBytes = kRawDepth * kRawBytes;
+  static constexpr int kEpiTurns = PAIR ? 2 : 1;       // staging buffers of an epilogue warp
+  static constexpr int kEpiWarpBytes = kEpiTurns * kPieceBytes;
+  static constexpr int kFixed = kStages * kStageBytes + 4 * kEpiWarpBytes + kSfBytes +
+                                kGroups * kRawGroupBytes + kGemmMisc;
+  static_assert(kFixed + 1024 + 8 * 2041 <= 232448, "shared memory of a block");
   static_assert(kAcc1 >= 0 && kAcc1 + kBN <= kSfCol, "tensor-memory columns overlap");
   static_assert(kOverlap % 64 == 0, "the overlap is drained in chunks of 64 columns");
 };
@@ -70,15 +80,17 @@ struct GemmCfg {
 struct GemmSmem {
   unsigned char* stages;
   unsigned char* epi;
-  unsigned char* sf;   // [2][8 words][A's rows, B's rows by 128][512] scale words
+  unsigned char* sf;   // [kChunk][A's rows, B's rows by 128][512] scale words
+  unsigned char* raw;  // [groups][kRawDepth][kRawBytes] the same as they arrive
   uint64_t* full;      // [kStages] (first SM of a pair) codes and scales are in
   uint64_t* empty;     // [kStages] the stage's MMAs are done
+  uint64_t* raw_full;  // [groups][kRawDepth] a chunk of scales has arrived
   uint64_t* d_full;    // [2] an accumulator holds a finished tile
   uint64_t* d_empty;   // [2] (first SM) its columns may be overwritten
   int* misc;           // [0] tensor-memory base, [1] abort
   int* scan;           // [10] warp totals
   int* ro;             // [E + 1] the row offsets (below 2^30)
-  int* pre;            // [E + 1] row tiles before each expert (not wgrad)
+  int* pre;            // [E + 1] row tiles before each expert; wgrad: scale rows before it
 };
 
 __device__ __forceinline__ bool gemm_aborted(const GemmSmem& m) {
@@ -100,342 +112,404 @@ struct GemmTile {
   int krows;       // wgrad: rows of the group
 };
 
+// Walks the tiles first, first + step, ...: columns fastest, then rows.
 template <typename C>
-__device__ __forceinline__ GemmTile gemm_tile(const GroupedGemmParams& p, const GemmSmem& m,
-                                              int t, int rank) {
-  GemmTile r;
-  const int nt = (p.N + C::kBN - 1) / C::kBN;
-  const int mt = t / nt;
-  r.n0 = (t - mt * nt) * C::kBN;
-  if constexpr (C::kWgrad) {
-    const int ht = (p.R + C::kTM - 1) / C::kTM;
-    r.e = mt / ht;
-    r.row0 = (mt - r.e * ht) * C::kTM + 128 * rank;
-    r.rows = max(0, min(128, p.R - (int)r.row0));
-    r.k0 = m.ro[r.e];
-    r.krows = m.ro[r.e + 1] - (int)r.k0;
-    r.kb = (r.krows + 31) >> 5;
-  } else {
-    int lo = 0, hi = p.E - 1;   // largest e with pre[e] <= mt (then mt < pre[e + 1])
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (m.pre[mid] <= mt) lo = mid; else hi = mid - 1;
-    }
-    r.e = lo;
-    r.row0 = m.ro[lo] + (mt - m.pre[lo]) * C::kTM + 128 * rank;
-    r.rows = max(0, min(128, m.ro[lo + 1] - (int)r.row0));
-    r.k0 = 0;
-    r.krows = 0;
-    r.kb = p.K >> 5;
+struct GemmWalk {
+  int t, tiles, step;
+  int nt, ni, dn;      // column tiles; this one; the step's
+  int mt, dm;          // row tile over all groups; the step's
+  int e;
+
+  __device__ __forceinline__ GemmWalk(const GroupedGemmParams& p, int first, int step_, int tiles_)
+      : t(first), tiles(tiles_), step(step_), e(0) {
+    nt = (p.N + C::kBN - 1) / C::kBN;
+    mt = first / nt;
+    ni = first - mt * nt;
+    dm = step / nt;
+    dn = step - dm * nt;
   }
-  return r;
-}
+  __device__ __forceinline__ bool done() const { return t >= tiles; }
+  __device__ __forceinline__ void next() {
+    t += step;
+    mt += dm;
+    ni += dn;
+    if (ni >= nt) ni -= nt, ++mt;
+  }
+  __device__ __forceinline__ GemmTile tile(const GroupedGemmParams& p, const GemmSmem& m,
+                                           int rank) {
+    GemmTile r;
+    r.n0 = ni * C::kBN;
+    if constexpr (C::kWgrad) {
+      const int ht = (p.R + C::kTM - 1) / C::kTM;
+      e = mt / ht;
+      r.row0 = (mt - e * ht) * C::kTM + 128 * rank;
+      r.rows = max(0, min(128, p.R - (int)r.row0));
+      r.k0 = m.ro[e];
+      r.krows = m.ro[e + 1] - (int)r.k0;
+      r.kb = (r.krows + 31) >> 5;
+    } else {
+      int hi = p.E - 1;   // largest e with pre[e] <= mt (then mt < pre[e + 1])
+      while (e < hi) {
+        const int mid = (e + hi + 1) >> 1;
+        if (m.pre[mid] <= mt) e = mid; else hi = mid - 1;
+      }
+      r.row0 = m.ro[e] + (mt - m.pre[e]) * C::kTM + 128 * rank;
+      r.rows = max(0, min(128, m.ro[e + 1] - (int)r.row0));
+      r.k0 = 0;
+      r.krows = 0;
+      r.kb = p.K >> 5;
+    }
+    r.e = e;
+    return r;
+  }
+};
 
 // ------------------------------------------------------------ scales
 // A word holds the scales of four consecutive blocks of one row of an operand
 // (rows of the output); a stage needs one word (E4M3) or two (E2M1) per row.
-// A loading warp serves 128 rows of one operand: it keeps kChunk words of each
-// row in registers, two chunks ahead, and writes them to shared memory in
-// pieces of 128 words.
-constexpr int kChunk = 8;
-
-// Loads that stay where they are written: a chunk ahead of their use.
-__device__ __forceinline__ uint32_t ldg32(const uint8_t* a) {
-  uint32_t v;
-  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(a));
-  return v;
-}
-__device__ __forceinline__ uint4 ldg128(const uint8_t* a) {
-  uint4 v;
-  asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(a));
-  return v;
-}
-
-// How a warp fetches: fixed per operand and launch, so that no load meets
-// another path's registers (the loads are unconditional, at addresses clamped
-// into the array: what lies outside is never used, and a load under a
-// condition was waited for where the paths join, a chunk too early).
+// Warps 4-7 walk every tile in chunks of kChunk words.  A loading warp serves
+// 128 rows of one operand: bulk copies (where the layout has no 16-byte steps,
+// cp.async) bring its words to shared memory kRawDepth chunks ahead, whence it
+// puts a chunk's words into pieces of 128, in the order in which tensor memory
+// takes them; all four warps then write each stage's words there.  (Plain
+// loads into registers ahead of their use waited for one another, and their
+// unrolled code missed the instruction cache: 3 - 6 thousand cycles a chunk.)
 enum ScaleMode : int {
   kTiled = 0,       // 128 x 4 tiles
-  kRows32 = 1,      // row-major, a row's blocks a multiple of 32 bytes
-  kRows16 = 2,      // ... of 16
-  kRows4 = 3,       // ... of 4
-  kRowsAny = 4,     // ... any: aligned words, shifted into place
-  kCols = 5,        // row-major, blocks outermost
+  kRows16 = 1,      // row-major, a row's blocks a multiple of 16 bytes
+  kRows4 = 2,       // ... of 4
+  kRowsAny = 3,     // ... any: aligned words, shifted into place
+  kCols = 4,        // row-major, blocks outermost
 };
 
 // Where a warp's scales of a tile come from.
 struct ScaleSrc {
   const uint8_t* s;   // the operand's scales
   int64_t r0;         // rows: first row; columns: first scale row of the group
-  int64_t rows;       // rows: rows that exist
+  int n;              // rows or columns of the 128 that the tile uses (may be <= 0)
+  int64_t bytes;      // kRowsAny: the array's length
   int pitch;          // rows: bytes (blocks) of a row; columns: width
   int c0;             // columns: first column
-  int nb;             // columns: blocks of the summed index
+  int nb;             // blocks of the summed index
   int64_t tile0;      // tiled: index of the first 512-byte tile
   int words;          // words of the summed index
 };
 
 template <typename C>
-__device__ __forceinline__ ScaleSrc scale_src(const GroupedGemmParams& p, const GemmTile& t,
-                                              int group) {
+__device__ __forceinline__ ScaleSrc scale_src(const GroupedGemmParams& p, const GemmSmem& m,
+                                              const GemmTile& t, int group) {
   ScaleSrc r;
   const bool a = group == 0;
   r.s = a ? p.a_scales : p.b_scales;
-  r.r0 = r.rows = r.tile0 = 0;
+  r.r0 = r.tile0 = r.bytes = 0;
   r.pitch = p.K >> 5;
-  r.c0 = r.nb = 0;
+  r.c0 = 0;
+  r.nb = t.kb;
   if (C::kAmn) {
-    r.r0 = p.cb_offs[t.e];
+    r.r0 = m.pre[t.e];   // (wgrad: the scale rows before each group)
     r.pitch = a ? p.R : p.N;
     r.c0 = a ? (int)t.row0 : t.n0 + 128 * (group - 1);
-    r.nb = t.kb;
+    r.n = r.pitch - r.c0;
     // the group's [width, blocks] matrix starts at byte k0 / 32 * width
     r.tile0 = ((t.k0 >> 5) * r.pitch >> 9) +
               (int64_t)(min(r.c0, r.pitch - 1) >> 7) * (t.krows >> 7);
   } else if (a) {
     r.r0 = t.row0;
-    r.rows = p.M;
+    r.n = t.rows;
+    r.bytes = p.M * r.pitch;
   } else if (C::kBmn) {
     // W quantised as one [E K, N] matrix in blocks of 32 rows
-    r.nb = r.pitch;
-    r.r0 = (int64_t)t.e * r.nb;
-    r.pitch = p.N;
+    r.r0 = (int64_t)t.e * r.pitch;
+    r.tile0 = r.r0 >> 2;
     r.c0 = t.n0 + 128 * (group - 1);
-    r.tile0 = (int64_t)(min(r.c0, r.pitch - 1) >> 7) * (((int64_t)p.E * r.nb) >> 2) + (r.r0 >> 2);
+    r.tile0 += (int64_t)(min(r.c0, p.N - 1) >> 7) * (((int64_t)p.E * r.pitch) >> 2);
+    r.pitch = p.N;
+    r.n = p.N - r.c0;
   } else {
     r.r0 = (int64_t)t.e * p.N + t.n0 + 128 * (group - 1);
-    r.rows = (int64_t)p.E * p.N;
+    r.n = p.N - t.n0 - 128 * (group - 1);
+    r.bytes = (int64_t)p.E * p.N * r.pitch;
   }
   r.words = (t.kb + 3) >> 2;
   return r;
 }
 
-// Words u .. u + kChunk - 1 of the warp's 128 rows.  Tiled, and row-major with
-// the summed index inside the rows: w[i][j] is row 32 j + lane's (kRowsAny:
-// the aligned words that hold them, one more per row).  kCols: w[i][j] holds
-// columns c0 + 4 lane .. + 3 of block 4 (u + i) + j.
-template <int MODE, bool OUTER>
-__device__ __forceinline__ void fetch_scales(const ScaleSrc& c, int u, int lane,
-                                             uint32_t (*w)[4]) {
-  const int last = c.words - 1;
-  if constexpr (MODE == kTiled && OUTER) {
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-      const uint4 v = ldg128(c.s + ((c.tile0 + min(u + i, last)) << 9) + 16 * lane);
-      w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
-    }
-  } else if constexpr (MODE == kTiled) {
-    // row by row: a group's first row need not be a tile's
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t r = min(c.r0 + 32 * j + lane, c.rows - 1);
-      const uint8_t* a = c.s + ((r >> 7) * c.words << 9) + ((r & 31) << 4) + (((r >> 5) & 3) << 2);
-#pragma unroll
-      for (int i = 0; i < kChunk; ++i) w[i][j] = ldg32(a + 512 * min(u + i, last));
-    }
-  } else if constexpr (MODE == kCols) {
-    const uint8_t* a = c.s + c.r0 * c.pitch + min(c.c0 + 4 * lane, c.pitch - 4);
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[i][j] = ldg32(a + (int64_t)min(4 * (u + i) + j, c.nb - 1) * c.pitch);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t r = min(c.r0 + 32 * j + lane, c.rows - 1);
-      const uint8_t* a = c.s + r * c.pitch;
-      if constexpr (MODE == kRows32) {
-        // a whole sector in one load: the operand tiles' stream leaves few
-        // request slots
-        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(w[0][j]), "=r"(w[1][j]), "=r"(w[2][j]), "=r"(w[3][j]),
-                       "=r"(w[4][j]), "=r"(w[5][j]), "=r"(w[6][j]), "=r"(w[7][j])
-                     : "l"(a + 4 * u));
-      } else if constexpr (MODE == kRows16) {
-#pragma unroll
-        for (int i = 0; i < kChunk; i += 4) {
-          const uint4 v = ldg128(a + 4 * min(u + i, last - 3));
-          w[i][j] = v.x, w[i + 1][j] = v.y, w[i + 2][j] = v.z, w[i + 3][j] = v.w;
-        }
-      } else if constexpr (MODE == kRows4) {
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) w[i][j] = ldg32(a + 4 * min(u + i, last));
-      } else {
-        // the array starts on a word; a word that holds one of its bytes is
-        // read whole
-        const int64_t end = (c.rows * c.pitch - 1) >> 2, at = (r * c.pitch + 4 * u) >> 2;
-#pragma unroll
-        for (int i = 0; i <= kChunk; ++i) w[i][j] = ldg32(c.s + 4 * min(at + i, end));
-      }
-    }
-  }
+__device__ __forceinline__ void copy4(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// A piece of 128 words in shared memory.  A's: row r's word at byte 4 r (each
-// warp reads its own 32).  B's: row 32 j + l's at byte 16 l + 4 j (a lane reads
-// its four).
-template <bool A, int MODE>
-__device__ __forceinline__ void put_words(unsigned char* dst, int lane, const uint32_t* x) {
-  uint32_t w[4] = {x[0], x[1], x[2], x[3]};
-  if constexpr (MODE == kCols) {
-    // four blocks of four columns a lane: a 4 x 4 byte transpose
-    const uint32_t t0 = __byte_perm(x[0], x[1], 0x5140), t1 = __byte_perm(x[2], x[3], 0x5140);
-    const uint32_t t2 = __byte_perm(x[0], x[1], 0x7362), t3 = __byte_perm(x[2], x[3], 0x7362);
-    w[0] = __byte_perm(t0, t1, 0x5410), w[1] = __byte_perm(t0, t1, 0x7632);
-    w[2] = __byte_perm(t2, t3, 0x5410), w[3] = __byte_perm(t2, t3, 0x7632);
+// Starts the copies of words u .. of the warp's 128 rows into `raw` (those of
+// the chunk that exist; rows that the tile does not use are left out as far as
+// that is cheap: with every SM of a decoding step reading the scales of a few
+// rows' neighbours too, the weights arrived a third slower).  Every lane
+// arrives once on `bar`, with or after its copies.
+template <int MODE, bool OUTER, int BOX>
+__device__ __forceinline__ void start_chunk(const ScaleSrc& c, const void* tmap, int u, int lane,
+                                            unsigned char* raw, uint64_t* bar) {
+  const int n = c.n > 0 ? min(kChunk, c.words - u) : 0;
+  const uint32_t dst = smem_addr(raw);
+  if constexpr (MODE == kCols || MODE == kRows16) {
+    if (lane == 0) {
+      // 32 block rows of 128 columns, or 32 bytes of up to 128 rows
+      const int boxes = n == 0 ? 0 : MODE == kCols ? 1 : (min(128, c.n) + BOX - 1) / BOX;
+      mbar_expect_tx(bar, boxes * (MODE == kCols ? 4096 : 32 * BOX));
+      for (int i = 0; i < boxes; ++i)
+        tc::load_2d<1>(raw + 32 * BOX * i, tmap, MODE == kCols ? c.c0 : 4 * u,
+                       MODE == kCols ? (int)c.r0 + 4 * u : (int)c.r0 + BOX * i, smem_addr(bar));
+      return;
+    }
+  } else if (MODE == kTiled && (OUTER || (c.r0 & 127) == 0)) {
+    if (lane == 0) {   // the rows are a tile's: its words lie one after another
+      const int64_t tile = OUTER ? c.tile0 : (c.r0 >> 7) * c.words;
+      mbar_expect_tx(bar, 512 * n);
+      if (n > 0) bulk_load(raw, c.s + ((tile + u) << 9), 512 * n, bar);
+      return;
+    }
+  } else {
+    const int rows = n == 0 ? 0 : min(128, c.n);
+    if constexpr (MODE == kTiled) {
+      for (int i = lane; i < rows; i += 32) {
+        const int64_t r = c.r0 + i;
+        const uint8_t* a = c.s + (((r >> 7) * c.words + u) << 9) + ((r & 31) << 4) +
+                           (((r >> 5) & 3) << 2);
+        for (int k = 0; k < n; ++k)
+          copy4(dst + 512 * k + 16 * (i & 31) + 4 * (i >> 5), a + 512 * k);
+      }
+    } else {
+      // up to nine words a row, neighbouring lanes a row's (kRowsAny: aligned
+      // words that hold its eight; the array starts on a word, and a word that
+      // holds one of its bytes is read whole)
+      constexpr int kPer = MODE == kRowsAny ? 9 : 8;
+      const int64_t end = (c.bytes - 1) >> 2;
+      for (int t = lane; t < kPer * rows; t += 32) {
+        const int r = t / kPer, i = t - kPer * r;
+        const int64_t at = ((c.r0 + r) * c.pitch + 4 * u) >> 2;
+        if (i < n + kPer - 8) copy4(dst + 36 * r + 4 * i, c.s + 4 * min(at + i, end));
+      }
+    }
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+    return;
   }
-  if constexpr (A != (MODE == kCols)) {
-    // A, rows 32 j + lane: word 32 j + lane; B, columns 4 lane + j: stored in
-    // the order j = (k + lane / 2) mod 4, so that each store's 32 words fall
-    // into different banks
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// A piece of 128 words.  A's: row r's at byte 4 r (each warp reads its own
+// 32).  B's: row 32 j + l's at byte 16 l + 4 j (a lane reads its four).
+template <bool A>
+__device__ __forceinline__ void put_rows(unsigned char* dst, int lane, uint32_t w0, uint32_t w1,
+                                         uint32_t w2, uint32_t w3) {
+  if constexpr (A) {
+    uint32_t* d = reinterpret_cast<uint32_t*>(dst) + lane;
+    d[0] = w0, d[32] = w1, d[64] = w2, d[96] = w3;
+  } else {
+    *reinterpret_cast<uint4*>(dst + 16 * lane) = make_uint4(w0, w1, w2, w3);
+  }
+}
+// The same from four blocks of columns 4 lane .. + 3: a 4 x 4 byte transpose;
+// for B the words are stored in the order (k + lane / 2) mod 4, so that each
+// store's 32 fall into different banks.
+template <bool A>
+__device__ __forceinline__ void put_cols(unsigned char* dst, int lane, uint32_t x0, uint32_t x1,
+                                         uint32_t x2, uint32_t x3) {
+  const uint32_t t0 = __byte_perm(x0, x1, 0x5140), t1 = __byte_perm(x2, x3, 0x5140);
+  const uint32_t t2 = __byte_perm(x0, x1, 0x7362), t3 = __byte_perm(x2, x3, 0x7362);
+  const uint32_t w0 = __byte_perm(t0, t1, 0x5410), w1 = __byte_perm(t0, t1, 0x7632);
+  const uint32_t w2 = __byte_perm(t2, t3, 0x5410), w3 = __byte_perm(t2, t3, 0x7632);
+  if constexpr (A) {
+    *reinterpret_cast<uint4*>(dst + 16 * lane) = make_uint4(w0, w1, w2, w3);
+  } else {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if constexpr (A) {
-        *reinterpret_cast<uint32_t*>(dst + 4 * (32 * k + lane)) = w[k];
-      } else {
-        const int j = (k + (lane >> 1)) & 3;
-        const uint32_t v = j & 2 ? (j & 1 ? w[3] : w[2]) : (j & 1 ? w[1] : w[0]);
-        *reinterpret_cast<uint32_t*>(dst + (4 * (lane & 7) + j) * 16 + (lane >> 3) * 4) = v;
-      }
+      const int j = (k + (lane >> 1)) & 3;
+      const uint32_t v = j & 2 ? (j & 1 ? w3 : w2) : (j & 1 ? w1 : w0);
+      *reinterpret_cast<uint32_t*>(dst + (4 * (lane & 7) + j) * 16 + (lane >> 3) * 4) = v;
     }
-  } else {
-    *reinterpret_cast<uint4*>(dst + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
-// One of warps 4-7.  LOADER: it fetches a group of 128 rows' words (group 0:
-// A's) two chunks ahead.  All four write every stage's words from shared into
-// tensor memory (tcgen05.st: a tcgen05.cp would take the tensor pipe's time),
-// warp q lanes 32 q .. 32 q + 31: lane l's A word, row 32 q + l's, in column q
-// of four; B column c, row 32 c + l's word.
+// A chunk that has arrived: its words into the warp's pieces.
+template <int MODE, bool OUTER, bool A, int STRIDE>
+__device__ __forceinline__ void put_chunk(const ScaleSrc& c, int u, int lane,
+                                          const unsigned char* raw, unsigned char* sf) {
+  const int n = min(kChunk, c.words - u);
+  if constexpr (MODE == kTiled) {
+    for (int i = 0; i < n; ++i) {
+      const uint4 v = *reinterpret_cast<const uint4*>(raw + 512 * i + 16 * lane);
+      put_rows<A>(sf + STRIDE * i, lane, v.x, v.y, v.z, v.w);
+    }
+  } else if constexpr (MODE == kCols) {
+    for (int i = 0; i < n; ++i) {
+      const uint32_t* x = reinterpret_cast<const uint32_t*>(raw + 512 * i) + lane;
+      put_cols<A>(sf + STRIDE * i, lane, x[0], x[32], x[64], x[96]);
+    }
+  } else if constexpr (MODE == kRowsAny || MODE == kRows4) {
+    int sh[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      sh[j] = 8 * (int)(((c.r0 + 32 * j + lane) * c.pitch) & 3);
+    for (int i = 0; i < n; ++i) {
+      // bytes past the row's end are another row's: a NaN scale there would
+      // meet the zeros of half an E2M1 step
+      const int have = min(4, c.pitch - 4 * (u + i));
+      const uint32_t mask = have < 4 ? (1u << (8 * have)) - 1u : ~0u;
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t* x = reinterpret_cast<const uint32_t*>(raw + 36 * (32 * j + lane)) + i;
+        w[j] = MODE == kRows4 ? x[0] : __funnelshift_r(x[0], x[1], sh[j]) & mask;
+      }
+      put_rows<A>(sf + STRIDE * i, lane, w[0], w[1], w[2], w[3]);
+    }
+  } else {
+    for (int h = 0; 4 * h < n; ++h) {
+      uint4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = *reinterpret_cast<const uint4*>(raw + 32 * (32 * j + lane) + 16 * h);
+      unsigned char* d = sf + STRIDE * 4 * h;
+      put_rows<A>(d, lane, v[0].x, v[1].x, v[2].x, v[3].x);
+      if (4 * h + 1 < n) put_rows<A>(d + STRIDE, lane, v[0].y, v[1].y, v[2].y, v[3].y);
+      if (4 * h + 2 < n) put_rows<A>(d + 2 * STRIDE, lane, v[0].z, v[1].z, v[2].z, v[3].z);
+      if (4 * h + 3 < n) put_rows<A>(d + 3 * STRIDE, lane, v[0].w, v[1].w, v[2].w, v[3].w);
+    }
+  }
+}
+
+// One of warps 4-7.  LOADER: it serves group `group` (0: A's rows).  Tensor
+// memory: lane l of quarter q, A's word of row 32 q + l in column q of four;
+// B's column c, row 32 c + l's word in lane l of every quarter.
 template <typename C, bool LOADER, bool OUTER, int MODE, bool A>
 __device__ __forceinline__ void gemm_scales(const GroupedGemmParams& p, const GemmSmem& m,
-                                            uint32_t tbase, int tiles, int first, int step,
+                                            const void* tmap, uint32_t tbase, int tiles, int first, int step,
                                             int rank, int group) {
   const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3;
   const uint32_t dst0 = tbase + ((uint32_t)(32 * q) << 16) + (uint32_t)C::kSfCol;
+  const uint32_t full0 = tc::leader_addr(m.full);
   constexpr int kStagesPerChunk = kChunk / C::kWords;
-  constexpr int kRegs = kChunk + (MODE == kRowsAny ? 1 : 0);
-  constexpr int kChunkBytes = kChunk * C::kGroups * 512;
-  int slot = 0, buf = 0;
-  uint32_t phase = 1;   // a fresh barrier's preceding phase counts as complete
-  // walks the chunks of every tile: chunk `chunk` of tile t
-  struct Walk { int t, chunk, left; };
-  auto next = [&](Walk& k, GemmTile& tile) {   // the next chunk's stages, 0 at the end
-    while (k.left <= 0) {
-      k.t += step;
-      if (k.t >= tiles) return 0;
-      tile = gemm_tile<C>(p, m, k.t, rank);
-      k.left = (tile.kb * 32 + C::kStageK - 1) / C::kStageK;
-      k.chunk = -1;
-    }
-    const int n = min(k.left, kStagesPerChunk);
-    k.left -= n;
-    ++k.chunk;
-    return n;
-  };
-  Walk load = {first - step, 0, 0}, serve = {first - step, 0, 0};
-  ScaleSrc src;
-  GemmTile load_tile, serve_tile;
-  struct Chunk { int word; int64_t r0; };   // what kRowsAny shifts and masks by
-  auto fetch = [&](uint32_t (*w)[4], Chunk& ch) {
+  constexpr int kStride = C::kGroups * 512;
+  unsigned char* raw = m.raw + group * C::kRawGroupBytes;
+  uint64_t* raw_full = m.raw_full + group * kRawDepth;
+  // the chunks to fetch, and their sources until they are put
+  GemmWalk<C> lw(p, first, step, tiles);
+  ScaleSrc src[kRawDepth];
+  int at[kRawDepth];
+  ScaleSrc cur;
+  int l_chunk = 0, l_words = 0;
+  static_assert(kRawDepth == 2, "two chunks on their way");
+  auto start = [&](ScaleSrc& sc, int& u, int buf) {   // the next chunk, if there is one
     if constexpr (LOADER) {
-      if (next(load, load_tile) == 0) return;
-      if (load.chunk == 0) src = scale_src<C>(p, load_tile, group);
-      fetch_scales<MODE, OUTER>(src, load.chunk * kChunk, lane, w);
-      ch.word = load.chunk * kChunk;
-      ch.r0 = src.r0;
-    }
-  };
-  auto one = [&](uint32_t (*w)[4], Chunk& ch) {
-    const int stages = next(serve, serve_tile);
-    if (stages == 0) return false;
-    unsigned char* sf = m.sf + buf * kChunkBytes;
-    if constexpr (LOADER) {
-      if constexpr (MODE == kRowsAny) {
-        const int pitch = src.pitch;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t r = min(ch.r0 + 32 * j + lane, src.rows - 1);
-          const int sh = 8 * (int)((r * pitch) & 3);
-#pragma unroll
-          for (int i = 0; i < kChunk; ++i) {
-            w[i][j] = __funnelshift_r(w[i][j], w[i + 1][j], sh);
-            // (bytes past the row's end are another row's: a NaN scale there
-            // would meet the zeros of half an E2M1 step)
-            if (4 * (ch.word + i) + 4 > pitch)
-              w[i][j] &= (1u << (8 * max(0, pitch - 4 * (ch.word + i)))) - 1u;
-          }
-        }
+      while (l_words <= 0) {   // the next tile with a sum to do
+        if (lw.done()) break;
+        const GemmTile t = lw.tile(p, m, rank);
+        lw.next();
+        l_words = (t.kb + 3) >> 2;
+        l_chunk = 0;
+        if (l_words > 0) cur = scale_src<C>(p, m, t, group);
       }
-#pragma unroll
-      for (int i = 0; i < kChunk; ++i)
-        if (i < stages * C::kWords) put_words<A, MODE>(sf + 512 * (C::kGroups * i + group), lane, w[i]);
-      fetch(w, ch);
+      if (l_words > 0) {
+        sc = cur;
+        u = l_chunk * kChunk;
+        start_chunk<MODE, OUTER, A ? C::kABox : 128>(sc, tmap, u, lane, raw + buf * kRawBytes,
+                                                     raw_full + buf);
+        l_words -= kChunk;
+        ++l_chunk;
+      }
     }
-    asm volatile("bar.sync 1, 128;" ::: "memory");   // the chunk is in shared memory
+  };
+  start(src[0], at[0], 0);
+  start(src[1], at[1], 1);
+  int slot = 0;
+  uint32_t phase = 1;   // a fresh barrier's preceding phase counts as complete
+  uint32_t raw_phase = 0;
+  auto serve = [&](ScaleSrc& sc, int& u, int buf, int stages) {
     bool ok = true;
+    if constexpr (LOADER) {
+      ok = __all_sync(kFull, tc::sleep(raw_full + buf, raw_phase));
+      if (buf == kRawDepth - 1) raw_phase ^= 1;
+      if (ok) put_chunk<MODE, OUTER, A, kStride>(sc, u, lane, raw + buf * kRawBytes,
+                                         m.sf + 512 * group);
+      __syncwarp();
+      start(sc, u, buf);
+    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");   // the chunk is in its pieces
+    // a stage's words are read before the wait for its slot, and the waits
+    // spin: the chain from a free slot to its scales in tensor memory bounds
+    // the rate of stages
+    uint32_t wa[C::kWords];
+    uint4 wb[C::kWords][C::kGroups - 1];
+    auto read = [&](int s) {
+#pragma unroll
+      for (int i = 0; i < C::kWords; ++i) {
+        const unsigned char* piece = m.sf + kStride * (s * C::kWords + i);
+        wa[i] = *reinterpret_cast<const uint32_t*>(piece + 4 * (32 * q + lane));
+#pragma unroll
+        for (int k = 1; k < C::kGroups; ++k)
+          wb[i][k - 1] = *reinterpret_cast<const uint4*>(piece + 512 * k + 16 * lane);
+      }
+    };
+    read(0);
     for (int s = 0; s < stages; ++s) {
-      ok = ok && __all_sync(kFull, tc::sleep(m.empty + slot, phase));
+      ok = ok && __all_sync(kFull, tc::spin(m.empty + slot, phase));
       if (ok) {
         tc::fence_after();
         const uint32_t dst = dst0 + slot * C::kSfPitch;
 #pragma unroll
         for (int i = 0; i < C::kWords; ++i) {
-          const unsigned char* piece = sf + 512 * C::kGroups * (s * C::kWords + i);
-          const uint32_t a = *reinterpret_cast<const uint32_t*>(piece + 4 * (32 * q + lane));
-          tc::st1(dst + 4 * i + q, a);
+          tc::st1(dst + 4 * i + q, wa[i]);
 #pragma unroll
-          for (int k = 1; k < C::kGroups; ++k) {
-            const uint4 b = *reinterpret_cast<const uint4*>(piece + 512 * k + 16 * lane);
-            tc::st4(dst + 4 * C::kWords + C::kSfbCols * i + 4 * (k - 1), b.x, b.y, b.z, b.w);
-          }
+          for (int k = 0; k < C::kGroups - 1; ++k)
+            tc::st4(dst + 4 * C::kWords + C::kSfbCols * i + 4 * k, wb[i][k].x, wb[i][k].y,
+                    wb[i][k].z, wb[i][k].w);
         }
         tc::wait_st();
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::arrive_cluster(tc::leader_addr(m.full + slot));
+        if (lane == 0) tc::arrive_cluster(full0 + 8 * slot);
       }
+      if (s + 1 < stages) read(s + 1);
       if (++slot == C::kStages) slot = 0, phase ^= 1;
     }
     if (!ok || gemm_aborted(m)) {
       ok = false;
       gemm_abort(p, m);
     }
-    buf ^= 1;
-    // the four warps leave together after an abort, at a barrier of their own
+    // every warp has read the pieces; after an abort they leave together
     int gone;
     asm volatile("{ .reg .pred p, r; setp.ne.s32 p, %1, 0; bar.red.or.pred r, 2, 128, p; "
                  "selp.s32 %0, 1, 0, r; }" : "=r"(gone) : "r"((int)!ok) : "memory");
     return gone == 0;
   };
-  uint32_t w0[kRegs][4], w1[kRegs][4];
-  Chunk c0, c1;
-  fetch(w0, c0);
-  fetch(w1, c1);
-  while (one(w0, c0) && one(w1, c1)) {
+  int buf = 0;
+  bool ok = true;
+  for (GemmWalk<C> w(p, first, step, tiles); ok && !w.done(); w.next()) {
+    int stages = (w.tile(p, m, rank).kb * 32 + C::kStageK - 1) / C::kStageK;
+    for (; ok && stages > 0; stages -= kStagesPerChunk) {
+      const int n = min(stages, kStagesPerChunk);
+      ok = buf == 0 ? serve(src[0], at[0], 0, n) : serve(src[1], at[1], 1, n);
+      buf ^= 1;
+    }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// The scale warp's role and loads, fixed for the launch.
+// The scale warp's role and copies, fixed for the launch.
 template <typename C>
 __device__ __forceinline__ void gemm_scales_any(const GroupedGemmParams& p, const GemmSmem& m,
+                                                const void* tm_sa, const void* tm_sb,
                                                 uint32_t tbase, int tiles, int first, int step,
                                                 int rank, int group) {
+  const void* tmap = group == 0 ? tm_sa : tm_sb;
   const bool tiled = group == 0 ? p.a_tiled : p.b_tiled;
   const int pitch = p.K >> 5;
 #define MOEACT_SCALES(OUTER, MODE, A) \
-  gemm_scales<C, true, OUTER, MODE, A>(p, m, tbase, tiles, first, step, rank, group)
+  gemm_scales<C, true, OUTER, MODE, A>(p, m, tmap, tbase, tiles, first, step, rank, group)
 #define MOEACT_SCALES_OF(OUTER, A)                             \
   if constexpr (OUTER) {                                       \
     if (tiled) MOEACT_SCALES(true, kTiled, A);                 \
     else MOEACT_SCALES(true, kCols, A);                        \
   } else {                                                     \
     if (tiled) MOEACT_SCALES(false, kTiled, A);                \
-    else if ((pitch & 31) == 0) MOEACT_SCALES(false, kRows32, A); \
     else if ((pitch & 15) == 0) MOEACT_SCALES(false, kRows16, A); \
     else if ((pitch & 3) == 0) MOEACT_SCALES(false, kRows4, A);   \
     else MOEACT_SCALES(false, kRowsAny, A);                    \
@@ -445,7 +519,7 @@ __device__ __forceinline__ void gemm_scales_any(const GroupedGemmParams& p, cons
   } else if (group < C::kGroups) {
     MOEACT_SCALES_OF(C::kBmn, false)
   } else {
-    gemm_scales<C, false, false, kRows32, false>(p, m, tbase, tiles, first, step, rank, group);
+    gemm_scales<C, false, false, kRows16, false>(p, m, tmap, tbase, tiles, first, step, rank, 0);
   }
 #undef MOEACT_SCALES_OF
 #undef MOEACT_SCALES
@@ -476,8 +550,8 @@ __device__ void gemm_producer(const GroupedGemmParams& p, const GemmSmem& m, con
   const bool leader = tc::elect_one();
   int slot = 0;
   uint32_t phase = 1;
-  for (int t = first; t < tiles; t += step) {
-    const GemmTile tile = gemm_tile<C>(p, m, t, rank);
+  for (GemmWalk<C> walk(p, first, step, tiles); !walk.done(); walk.next()) {
+    const GemmTile tile = walk.tile(p, m, rank);
     const int stages = (tile.kb * 32 + C::kStageK - 1) / C::kStageK;
     const int col_b = tile.n0 + (C::kCG == 2 ? 128 * rank : 0);   // this SM's rows of B
     for (int s = 0; s < stages; ++s) {
@@ -548,8 +622,8 @@ __device__ void gemm_mma(const GroupedGemmParams& p, const GemmSmem& m, uint32_t
   const uint64_t b0 = tc::desc_sw128(smem_addr(m.stages + kTileBytes));
   int slot = 0, n = 0;
   uint32_t phase = 0;
-  for (int t = first; t < tiles; t += step) {
-    const int kb = gemm_tile<C>(p, m, t, 0).kb;
+  for (GemmWalk<C> walk(p, first, step, tiles); !walk.done(); walk.next()) {
+    const int kb = walk.tile(p, m, 0).kb;
     if (kb == 0) continue;
     const int mmas = (kb * 32 + C::kMmaK - 1) / C::kMmaK;
     // the tile whose columns this one takes: the last but one, or with
@@ -594,23 +668,42 @@ __device__ void gemm_mma(const GroupedGemmParams& p, const GemmSmem& m, uint32_t
 
 // ------------------------------------------------------------ epilogue
 // 32 rows x 128 bytes from registers (thread t: row t, as eight 16-byte
-// pieces) through the warp's staging, so that each store writes whole row
-// segments.  `cols` output columns of the piece's 128 bytes exist.
-template <bool OUT32>
-__device__ __forceinline__ void store_piece(const GroupedGemmParams& p, unsigned char* stg,
-                                            const uint4* v, int64_t row, int rows, int col,
+// pieces) into the warp's staging, swizzled (piece c of row r at c ^ (r mod
+// 8)), and from there to the output: whole pieces by one bulk tensor store,
+// which clips columns past the output's and leaves the warp free (the TURNS
+// staging buffers take turns); pieces with fewer rows, and sums with what the output
+// holds, by plain stores of whole row segments.
+template <bool WGRAD, bool OUT32, int TURNS>
+__device__ __forceinline__ void store_piece(const GroupedGemmParams& p, const void* tm_out,
+                                            unsigned char* stg, int& turn, const uint4* v,
+                                            int64_t row, int rows, int col, int e, int e_row,
                                             int lane) {
   constexpr int kPer = OUT32 ? 4 : 8;   // columns in 16 bytes
+  unsigned char* buf = stg + turn * kPieceBytes;
+  if (TURNS > 1) turn ^= 1;
+  if (lane == 0) tc::bulk_wait_read<TURNS - 1>();   // this buffer's last store has read it
+  __syncwarp();
 #pragma unroll
   for (int c = 0; c < 8; ++c)
-    *reinterpret_cast<uint4*>(stg + lane * 128 + ((c ^ (lane & 7)) << 4)) = v[c];
+    *reinterpret_cast<uint4*>(buf + lane * 128 + ((c ^ (lane & 7)) << 4)) = v[c];
+  if ((WGRAD || rows == 32) && !p.accumulate) {
+    tc::fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) {
+      if constexpr (WGRAD) tc::store_3d(tm_out, buf, col, e_row, e);
+      else tc::store_2d(tm_out, buf, col, (int)row);
+      tc::bulk_commit();
+    }
+    __syncwarp();
+    return;
+  }
   __syncwarp();
   const int c = lane & 7;
   const bool in = col + kPer * c < p.N;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const int r = 4 * k + (lane >> 3);
-    uint4 w = *reinterpret_cast<const uint4*>(stg + r * 128 + ((c ^ (r & 7)) << 4));
+    uint4 w = *reinterpret_cast<const uint4*>(buf + r * 128 + ((c ^ (r & 7)) << 4));
     if (in && r < rows) {
       if constexpr (OUT32) {
         float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + (row + r) * p.ldo +
@@ -633,23 +726,31 @@ __device__ __forceinline__ void store_piece(const GroupedGemmParams& p, unsigned
 }
 
 template <typename C>
-__device__ void gemm_epilogue(const GroupedGemmParams& p, const GemmSmem& m, uint32_t tbase,
-                              int tiles, int first, int step, int rank) {
+__device__ void gemm_epilogue(const GroupedGemmParams& p, const GemmSmem& m, const void* tm_out,
+                              uint32_t tbase, int tiles, int first, int step, int rank) {
   const int q = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
-  unsigned char* stg = m.epi + q * kEpiWarpBytes;
-  int n = 0;
-  for (int t = first; t < tiles; t += step) {
-    const GemmTile tile = gemm_tile<C>(p, m, t, rank);
+  unsigned char* stg = m.epi + q * C::kEpiWarpBytes;
+  int n = 0, turn = 0;
+  for (GemmWalk<C> walk(p, first, step, tiles); !walk.done(); walk.next()) {
+    const GemmTile tile = walk.tile(p, m, rank);
     const int rows = max(0, min(32, tile.rows - 32 * q));
-    const int64_t row = (C::kWgrad ? (int64_t)tile.e * p.R : 0) + tile.row0 + 32 * q;
+    const int e_row = (int)tile.row0 + 32 * q;   // row of A, or (wgrad) of dW_e
+    const int64_t row = (C::kWgrad ? (int64_t)tile.e * p.R : 0) + e_row;
+    auto put = [&](auto out32, const uint4* v, int col) {
+      store_piece<C::kWgrad, decltype(out32)::value, C::kEpiTurns>(p, tm_out, stg, turn, v, row, rows, col,
+                                                     tile.e, e_row, lane);
+    };
+    using Bf16 = std::integral_constant<bool, false>;
+    using Fp32 = std::integral_constant<bool, true>;
     if (tile.kb == 0) {   // wgrad of an expert without rows: zeros
-      if (p.accumulate) continue;
+      if (p.accumulate || rows == 0) continue;
       uint4 z[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) z[i] = make_uint4(0u, 0u, 0u, 0u);
-      for (int c = 0; c < C::kBN; c += p.out32 ? 32 : 64) {
-        if (p.out32) store_piece<true>(p, stg, z, row, rows, tile.n0 + c, lane);
-        else store_piece<false>(p, stg, z, row, rows, tile.n0 + c, lane);
+      const int per = p.out32 ? 32 : 64;
+      for (int c = tile.n0; c < min(tile.n0 + C::kBN, p.N); c += per) {
+        if (p.out32) put(Fp32(), z, c);
+        else put(Bf16(), z, c);
       }
       continue;
     }
@@ -685,7 +786,7 @@ __device__ void gemm_epilogue(const GroupedGemmParams& p, const GemmSmem& m, uin
           for (int j = 0; j < 8; ++j)
             w[j] = make_uint4(v[32 * h + 4 * j], v[32 * h + 4 * j + 1], v[32 * h + 4 * j + 2],
                               v[32 * h + 4 * j + 3]);
-          store_piece<true>(p, stg, w, row, rows, col + 32 * h, lane);
+          if (col + 32 * h < p.N) put(Fp32(), w, col + 32 * h);
         }
       } else {
         uint4 w[8];
@@ -697,18 +798,23 @@ __device__ void gemm_epilogue(const GroupedGemmParams& p, const GemmSmem& m, uin
                             pack_bf16x2(__uint_as_float(x[4]), __uint_as_float(x[5])),
                             pack_bf16x2(__uint_as_float(x[6]), __uint_as_float(x[7])));
         }
-        store_piece<false>(p, stg, w, row, rows, col, lane);
+        put(Bf16(), w, col);
       }
     }
     ++n;
   }
+  if (lane == 0) tc::bulk_wait();   // the stores are out before the memory is given up
+  __syncwarp();
 }
 
 // ------------------------------------------------------------ kernel
 template <int OP, bool PAIR>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
-                        const __grid_constant__ CUtensorMap tm_b, const GroupedGemmParams p) {
+                        const __grid_constant__ CUtensorMap tm_b,
+                        const __grid_constant__ CUtensorMap tm_sa,
+                        const __grid_constant__ CUtensorMap tm_sb,
+                        const __grid_constant__ CUtensorMap tm_out, const GroupedGemmParams p) {
   using C = GemmCfg<OP, PAIR>;
   if (p.noop != nullptr && *p.noop != 0) return;
   extern __shared__ __align__(1024) unsigned char gemm_smem[];
@@ -716,17 +822,26 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   GemmSmem m;
   m.stages = base;
   m.epi = base + C::kStages * C::kStageBytes;
-  m.sf = m.epi + 4 * kEpiWarpBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(m.epi + 4 * kEpiWarpBytes + C::kSfBytes);
+  m.sf = m.epi + 4 * C::kEpiWarpBytes;
+  m.raw = m.sf + C::kSfBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(m.raw + C::kGroups * C::kRawGroupBytes);
   m.full = bars;
   m.empty = m.full + C::kStages;
-  m.d_full = m.empty + C::kStages;
+  m.raw_full = m.empty + C::kStages;
+  m.d_full = m.raw_full + C::kGroups * kRawDepth;
   m.d_empty = m.d_full + 2;
   m.misc = reinterpret_cast<int*>(bars + 64);
   m.scan = m.misc + 16;
   m.ro = reinterpret_cast<int*>(reinterpret_cast<unsigned char*>(bars) + kGemmMisc);
   m.pre = m.ro + p.E + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    tc::prefetch_map(&tm_a);
+    tc::prefetch_map(&tm_b);
+    if (!p.a_tiled) tc::prefetch_map(&tm_sa);
+    if (!p.b_tiled) tc::prefetch_map(&tm_sb);
+    tc::prefetch_map(&tm_out);
+  }
   const int rank = PAIR ? (int)tc::cluster_rank() : 0;
 
   // ---- the groups: offsets checked, row tiles before each expert
@@ -741,6 +856,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (r1 < r0 || r0 < 0 || r1 > p.M) bad |= 1;
     else local += (int)((r1 - r0 + C::kTM - 1) / C::kTM);
     if constexpr (C::kWgrad) {
+      m.pre[e] = (int)p.cb_offs[e];
       if (p.cb_offs[e + 1] - p.cb_offs[e] != (r1 - r0 + 31) >> 5) bad |= 1;
       if ((p.a_tiled || p.b_tiled) && ((r1 - r0) & 127) != 0) bad |= 2;
     }
@@ -782,6 +898,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       mbar_init(m.full + i, 5 * C::kCG);   // per SM: the TMA warp and four scale warps
       mbar_init(m.empty + i, 1);
     }
+    for (int i = 0; i < C::kGroups * kRawDepth; ++i) mbar_init(m.raw_full + i, 32);
     for (int i = 0; i < 2; ++i) {
       mbar_init(m.d_full + i, 1);
       mbar_init(m.d_empty + i, 4 * C::kCG);
@@ -799,8 +916,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   tc::fence_after();
   const uint32_t tbase = *reinterpret_cast<volatile uint32_t*>(m.misc);
 
-  if (warp < 4) gemm_epilogue<C>(p, m, tbase, tiles, first, step, rank);
-  else if (warp < 8) gemm_scales_any<C>(p, m, tbase, tiles, first, step, rank, warp - 4);
+  if (warp < 4) gemm_epilogue<C>(p, m, &tm_out, tbase, tiles, first, step, rank);
+  else if (warp < 8) 
+    gemm_scales_any<C>(p, m, &tm_sa, &tm_sb, tbase, tiles, first, step, rank, warp - 4);
   else if (warp == 8) gemm_producer<C>(p, m, &tm_a, &tm_b, tiles, first, step, rank);
   else if (rank == 0) gemm_mma<C>(p, m, tbase, tiles, first, step);
 
@@ -824,7 +942,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 template <int OP, bool PAIR>
 int gemm_smem_bytes(int E) {
   using C = GemmCfg<OP, PAIR>;
-  return 1024 + C::kFixed + (E + 1) * (C::kWgrad ? 4 : 8);
+  return 1024 + C::kFixed + (E + 1) * 8;
 }
 
 template <int OP, bool PAIR>
@@ -835,8 +953,8 @@ cudaError_t gemm_prepare_one(int max_groups) {
 }
 
 template <int OP, bool PAIR>
-cudaError_t gemm_launch_one(const GroupedGemmParams& p, const CUtensorMap& tm_a,
-                            const CUtensorMap& tm_b, int n_sms, cudaStream_t stream) {
+cudaError_t gemm_launch_one(const GroupedGemmParams& p, const GemmMaps& tm, int n_sms,
+                            cudaStream_t stream) {
   using C = GemmCfg<OP, PAIR>;
   // at most as many row tiles as full ones and one more per group
   const int64_t row_tiles = C::kWgrad ? (int64_t)p.E * ((p.R + C::kTM - 1) / C::kTM)
@@ -854,7 +972,8 @@ cudaError_t gemm_launch_one(const GroupedGemmParams& p, const CUtensorMap& tm_a,
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, grouped_gemm_kernel<OP, PAIR>, tm_a, tm_b, p);
+  return cudaLaunchKernelEx(&cfg, grouped_gemm_kernel<OP, PAIR>, tm.a, tm.b, tm.sa, tm.sb, tm.out,
+                            p);
 }
 
 }  // namespace
@@ -868,9 +987,8 @@ cudaError_t gemm_launch_one(const GroupedGemmParams& p, const CUtensorMap& tm_a,
     return e != cudaSuccess ? e : gemm_prepare_one<OP, true>(MOEACT_MAX_GROUPS);                \
   }                                                                                             \
   cudaError_t grouped_gemm_launch_##name(bool pair, const GroupedGemmParams& p,                 \
-                                         const CUtensorMap& tm_a, const CUtensorMap& tm_b,      \
-                                         int n_sms, cudaStream_t stream) {                      \
-    return pair ? gemm_launch_one<OP, true>(p, tm_a, tm_b, n_sms, stream)                       \
-                : gemm_launch_one<OP, false>(p, tm_a, tm_b, n_sms, stream);                     \
+                                         const GemmMaps& tm, int n_sms, cudaStream_t stream) {  \
+    return pair ? gemm_launch_one<OP, true>(p, tm, n_sms, stream)                               \
+                : gemm_launch_one<OP, false>(p, tm, n_sms, stream);                             \
   }                                                                                             \
   }
