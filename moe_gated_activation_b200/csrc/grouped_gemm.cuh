@@ -41,7 +41,7 @@ struct GroupedGemmParams {
   uint32_t* err;              // device error word
 };
 
-constexpr int kGemmThreads = 320;   // 4 epilogue, 4 scale, a TMA and an MMA warp
+constexpr int kGemmThreads = 352;   // 4 epilogue, 4 scale, a TMA, an MMA and a scale-loading warp
 // Rows of a tensor-map box: 128 (an SM's share of an operand tile), except 32
 // where fewer rows may be wanted: the A rows of the one-SM kernels, whose
 // groups can be short, and operands stored with the summed index outermost,

@@ -11,9 +11,9 @@
 // wave share the rows of A and one expert's W in L2).  Roles, per SM:
 //   warps 0-3  epilogue: accumulator -> registers -> rounding -> shared
 //              memory -> bulk tensor stores of 32 rows x 128 bytes;
-//   warps 4-7  scales: E8M0 words from global memory, in either layout, some
-//              chunks ahead into shared memory, and each stage's from there
-//              into tensor memory (tcgen05.st);
+//   warps 4-7  scales: E8M0 words from shared memory, as they came, into the
+//              order of tensor memory and each stage's there (tcgen05.st);
+//   warp 10    the scales' copies into shared memory, some chunks ahead;
 //   warp 8     TMA loads of the code tiles (128 rows x 128 bytes each);
 //   warp 9     tensor-memory allocation; in the pair's first SM the MMAs.
 // One ring of stages carries codes and scales: `full` collects the TMA bytes
@@ -85,10 +85,11 @@ struct GemmSmem {
   uint64_t* full;      // [kStages] (first SM of a pair) codes and scales are in
   uint64_t* empty;     // [kStages] the stage's MMAs are done
   uint64_t* raw_full;  // [groups][kRawDepth] a chunk of scales has arrived
+  uint64_t* raw_empty; // [kRawDepth] ... and is in its pieces
   uint64_t* d_full;    // [2] an accumulator holds a finished tile
   uint64_t* d_empty;   // [2] (first SM) its columns may be overwritten
   int* misc;           // [0] tensor-memory base, [1] abort
-  int* scan;           // [10] warp totals
+  int* scan;           // [11] warp totals
   int* ro;             // [E + 1] the row offsets (below 2^30)
   int* pre;            // [E + 1] row tiles before each expert; wgrad: scale rows before it
 };
@@ -167,11 +168,11 @@ struct GemmWalk {
 // ------------------------------------------------------------ scales
 // A word holds the scales of four consecutive blocks of one row of an operand
 // (rows of the output); a stage needs one word (E4M3) or two (E2M1) per row.
-// Warps 4-7 walk every tile in chunks of kChunk words.  A loading warp serves
-// 128 rows of one operand: bulk copies (where the layout has no 16-byte steps,
-// cp.async) bring its words to shared memory kRawDepth chunks ahead, whence it
-// puts a chunk's words into pieces of 128, in the order in which tensor memory
-// takes them; all four warps then write each stage's words there.  (Plain
+// They go in chunks of kChunk words: bulk copies (where the layout has no
+// 16-byte steps, cp.async) bring a chunk to shared memory kRawDepth chunks
+// ahead; warps 4, 5 (and 6) each put one group of 128 rows' words into pieces
+// of 128, in the order in which tensor memory takes them; warps 4-7 then write
+// each stage's words there.  (Plain
 // loads into registers ahead of their use waited for one another, and their
 // unrolled code missed the instruction cache: 3 - 6 thousand cycles a chunk.)
 enum ScaleMode : int {
@@ -180,6 +181,7 @@ enum ScaleMode : int {
   kRows4 = 2,       // ... of 4
   kRowsAny = 3,     // ... any: aligned words, shifted into place
   kCols = 4,        // row-major, blocks outermost
+  kFlat = 5,        // row-major, a row's blocks in one chunk: 128 rows in one piece
 };
 
 // Where a warp's scales of a tile come from.
@@ -187,7 +189,7 @@ struct ScaleSrc {
   const uint8_t* s;   // the operand's scales
   int64_t r0;         // rows: first row; columns: first scale row of the group
   int n;              // rows or columns of the 128 that the tile uses (may be <= 0)
-  int64_t bytes;      // kRowsAny: the array's length
+  int64_t bytes;      // rows: the array's length
   int pitch;          // rows: bytes (blocks) of a row; columns: width
   int c0;             // columns: first column
   int nb;             // blocks of the summed index
@@ -238,24 +240,30 @@ __device__ __forceinline__ void copy4(uint32_t dst, const uint8_t* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// `have` bytes (1 .. 16) and zeros to 16.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, int have) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have)
+               : "memory");
+}
+
 // Starts the copies of words u .. of the warp's 128 rows into `raw` (those of
 // the chunk that exist; rows that the tile does not use are left out as far as
 // that is cheap: with every SM of a decoding step reading the scales of a few
 // rows' neighbours too, the weights arrived a third slower).  Every lane
 // arrives once on `bar`, with or after its copies.
-template <int MODE, bool OUTER, int BOX>
-__device__ __forceinline__ void start_chunk(const ScaleSrc& c, const void* tmap, int u, int lane,
-                                            unsigned char* raw, uint64_t* bar) {
+template <int MODE, bool OUTER>
+__device__ __forceinline__ void start_chunk(const ScaleSrc& c, const void* tmap, int box_rows,
+                                            int u, int lane, unsigned char* raw, uint64_t* bar) {
   const int n = c.n > 0 ? min(kChunk, c.words - u) : 0;
   const uint32_t dst = smem_addr(raw);
   if constexpr (MODE == kCols || MODE == kRows16) {
     if (lane == 0) {
       // 32 block rows of 128 columns, or 32 bytes of up to 128 rows
-      const int boxes = n == 0 ? 0 : MODE == kCols ? 1 : (min(128, c.n) + BOX - 1) / BOX;
-      mbar_expect_tx(bar, boxes * (MODE == kCols ? 4096 : 32 * BOX));
+      const int boxes = n == 0 ? 0 : MODE == kCols ? 1 : box_rows == 128 ? 1 : (min(128, c.n) + 31) / 32;
+      mbar_expect_tx(bar, boxes * (MODE == kCols ? 4096 : 32 * box_rows));
       for (int i = 0; i < boxes; ++i)
-        tc::load_2d<1>(raw + 32 * BOX * i, tmap, MODE == kCols ? c.c0 : 4 * u,
-                       MODE == kCols ? (int)c.r0 + 4 * u : (int)c.r0 + BOX * i, smem_addr(bar));
+        tc::load_2d<1>(raw + 1024 * i, tmap, MODE == kCols ? c.c0 : 4 * u,
+                       MODE == kCols ? (int)c.r0 + 4 * u : (int)c.r0 + 32 * i, smem_addr(bar));
       return;
     }
   } else if (MODE == kTiled && (OUTER || (c.r0 & 127) == 0)) {
@@ -267,7 +275,14 @@ __device__ __forceinline__ void start_chunk(const ScaleSrc& c, const void* tmap,
     }
   } else {
     const int rows = n == 0 ? 0 : min(128, c.n);
-    if constexpr (MODE == kTiled) {
+    if constexpr (MODE == kFlat) {
+      const int64_t at = c.r0 * c.pitch & ~(int64_t)15;
+      const int all = (int)(c.r0 * c.pitch - at) + rows * c.pitch;
+      const int64_t left = c.bytes - at;
+      if (rows > 0)
+        for (int t = 16 * lane; t < all; t += 512)
+          copy16(dst + t, c.s + at + t, (int)min((int64_t)16, left - t));
+    } else if constexpr (MODE == kTiled) {
       for (int i = lane; i < rows; i += 32) {
         const int64_t r = c.r0 + i;
         const uint8_t* a = c.s + (((r >> 7) * c.words + u) << 9) + ((r & 31) << 4) +
@@ -291,7 +306,7 @@ __device__ __forceinline__ void start_chunk(const ScaleSrc& c, const void* tmap,
                  : "memory");
     return;
   }
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+  tc::arrive(bar);
 }
 
 // A piece of 128 words.  A's: row r's at byte 4 r (each warp reads its own
@@ -329,7 +344,7 @@ __device__ __forceinline__ void put_cols(unsigned char* dst, int lane, uint32_t 
 }
 
 // A chunk that has arrived: its words into the warp's pieces.
-template <int MODE, bool OUTER, bool A, int STRIDE>
+template <int MODE, bool A, int STRIDE>
 __device__ __forceinline__ void put_chunk(const ScaleSrc& c, int u, int lane,
                                           const unsigned char* raw, unsigned char* sf) {
   const int n = min(kChunk, c.words - u);
@@ -343,11 +358,17 @@ __device__ __forceinline__ void put_chunk(const ScaleSrc& c, int u, int lane,
       const uint32_t* x = reinterpret_cast<const uint32_t*>(raw + 512 * i) + lane;
       put_cols<A>(sf + STRIDE * i, lane, x[0], x[32], x[64], x[96]);
     }
-  } else if constexpr (MODE == kRowsAny || MODE == kRows4) {
-    int sh[4];
+  } else if constexpr (MODE == kRowsAny || MODE == kFlat) {   // (and kRows4)
+    int sh[4], at[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      sh[j] = 8 * (int)(((c.r0 + 32 * j + lane) * c.pitch) & 3);
+    for (int j = 0; j < 4; ++j) {
+      const int r = 32 * j + lane;
+      at[j] = MODE == kFlat ? (int)(c.r0 * c.pitch & 15) + r * c.pitch
+                            : 36 * r + (int)((c.r0 + r) * c.pitch & 3);
+      sh[j] = 8 * (at[j] & 3);
+      at[j] >>= 2;
+    }
+#pragma unroll 2
     for (int i = 0; i < n; ++i) {
       // bytes past the row's end are another row's: a NaN scale there would
       // meet the zeros of half an E2M1 step
@@ -356,8 +377,8 @@ __device__ __forceinline__ void put_chunk(const ScaleSrc& c, int u, int lane,
       uint32_t w[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t* x = reinterpret_cast<const uint32_t*>(raw + 36 * (32 * j + lane)) + i;
-        w[j] = MODE == kRows4 ? x[0] : __funnelshift_r(x[0], x[1], sh[j]) & mask;
+        const uint32_t* x = reinterpret_cast<const uint32_t*>(raw) + at[j] + i;
+        w[j] = __funnelshift_r(x[0], x[1], sh[j]) & mask;
       }
       put_rows<A>(sf + STRIDE * i, lane, w[0], w[1], w[2], w[3]);
     }
@@ -376,12 +397,74 @@ __device__ __forceinline__ void put_chunk(const ScaleSrc& c, int u, int lane,
   }
 }
 
-// One of warps 4-7.  LOADER: it serves group `group` (0: A's rows).  Tensor
-// memory: lane l of quarter q, A's word of row 32 q + l in column q of four;
-// B's column c, row 32 c + l's word in lane l of every quarter.
-template <typename C, bool LOADER, bool OUTER, int MODE, bool A>
+__device__ __forceinline__ int scale_mode(bool outer, bool tiled, int pitch) {
+  return tiled ? kTiled
+         : outer ? kCols
+         : (pitch & 15) == 0 ? kRows16
+         : pitch <= 4 * kChunk ? kFlat
+         : (pitch & 3) == 0 ? kRows4 : kRowsAny;
+}
+
+// Warp 10: the copies of every chunk of every group, kRawDepth ahead.  (In a
+// warp of its own: the setting up of a tile's copies -- a search for the
+// group, 64-bit addresses, cold code -- took one to three thousand cycles out
+// of the warps that feed tensor memory.)
+template <typename C>
+__device__ void gemm_scale_loader(const GroupedGemmParams& p, const GemmSmem& m,
+                                  const void* tm_sa, const void* tm_sb, int tiles, int first,
+                                  int step, int rank) {
+  const int lane = threadIdx.x & 31;
+  const int mode_a = scale_mode(C::kAmn, p.a_tiled, p.K >> 5);
+  const int mode_b = scale_mode(C::kBmn, p.b_tiled, p.K >> 5);
+  int buf = 0;
+  uint32_t phase = 1;
+  for (GemmWalk<C> w(p, first, step, tiles); !w.done(); w.next()) {
+    const GemmTile t = w.tile(p, m, rank);
+    const int words = (t.kb + 3) >> 2;
+    for (int u = 0; u < words; u += kChunk) {
+      if (!__all_sync(kFull, tc::sleep(m.raw_empty + buf, phase)) || gemm_aborted(m)) {
+        gemm_abort(p, m);
+        return;
+      }
+#pragma unroll 1
+      for (int g = 0; g < C::kGroups; ++g) {
+        const ScaleSrc src = scale_src<C>(p, m, t, g);
+        unsigned char* raw = m.raw + g * C::kRawGroupBytes + buf * kRawBytes;
+        uint64_t* bar = m.raw_full + g * kRawDepth + buf;
+        const int mode = g == 0 ? mode_a : mode_b;
+        const void* tmap = g == 0 ? tm_sa : tm_sb;
+        const int box = g == 0 ? C::kABox : 128;
+        if constexpr (C::kBmn) {
+          if (g > 0 || C::kAmn) {
+            if (mode == kCols) start_chunk<kCols, true>(src, tmap, box, u, lane, raw, bar);
+            else start_chunk<kTiled, true>(src, tmap, box, u, lane, raw, bar);
+            continue;
+          }
+        }
+        if constexpr (!C::kAmn) {
+          switch (mode) {
+            case kTiled: start_chunk<kTiled, false>(src, tmap, box, u, lane, raw, bar); break;
+            case kRows16: start_chunk<kRows16, false>(src, tmap, box, u, lane, raw, bar); break;
+            case kFlat: start_chunk<kFlat, false>(src, tmap, box, u, lane, raw, bar); break;
+            case kRows4: start_chunk<kRows4, false>(src, tmap, box, u, lane, raw, bar); break;
+            default: start_chunk<kRowsAny, false>(src, tmap, box, u, lane, raw, bar);
+          }
+        }
+      }
+      __syncwarp();
+      if (++buf == kRawDepth) buf = 0, phase ^= 1;
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// One of warps 4-7.  PUT: it puts group `group`'s (0: A's rows) words into
+// pieces.  Tensor memory: lane l of quarter q, A's word of row 32 q + l in
+// column q of four; B's column c, row 32 c + l's word in lane l of every
+// quarter.
+template <typename C, bool PUT, int MODE, bool A>
 __device__ __forceinline__ void gemm_scales(const GroupedGemmParams& p, const GemmSmem& m,
-                                            const void* tmap, uint32_t tbase, int tiles, int first, int step,
+                                            uint32_t tbase, int tiles, int first, int step,
                                             int rank, int group) {
   const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3;
   const uint32_t dst0 = tbase + ((uint32_t)(32 * q) << 16) + (uint32_t)C::kSfCol;
@@ -390,48 +473,18 @@ __device__ __forceinline__ void gemm_scales(const GroupedGemmParams& p, const Ge
   constexpr int kStride = C::kGroups * 512;
   unsigned char* raw = m.raw + group * C::kRawGroupBytes;
   uint64_t* raw_full = m.raw_full + group * kRawDepth;
-  // the chunks to fetch, and their sources until they are put
-  GemmWalk<C> lw(p, first, step, tiles);
-  ScaleSrc src[kRawDepth];
-  int at[kRawDepth];
-  ScaleSrc cur;
-  int l_chunk = 0, l_words = 0;
-  static_assert(kRawDepth == 2, "two chunks on their way");
-  auto start = [&](ScaleSrc& sc, int& u, int buf) {   // the next chunk, if there is one
-    if constexpr (LOADER) {
-      while (l_words <= 0) {   // the next tile with a sum to do
-        if (lw.done()) break;
-        const GemmTile t = lw.tile(p, m, rank);
-        lw.next();
-        l_words = (t.kb + 3) >> 2;
-        l_chunk = 0;
-        if (l_words > 0) cur = scale_src<C>(p, m, t, group);
-      }
-      if (l_words > 0) {
-        sc = cur;
-        u = l_chunk * kChunk;
-        start_chunk<MODE, OUTER, A ? C::kABox : 128>(sc, tmap, u, lane, raw + buf * kRawBytes,
-                                                     raw_full + buf);
-        l_words -= kChunk;
-        ++l_chunk;
-      }
-    }
-  };
-  start(src[0], at[0], 0);
-  start(src[1], at[1], 1);
   int slot = 0;
   uint32_t phase = 1;   // a fresh barrier's preceding phase counts as complete
   uint32_t raw_phase = 0;
-  auto serve = [&](ScaleSrc& sc, int& u, int buf, int stages) {
+  auto serve = [&](const ScaleSrc& sc, int u, int buf, int stages) {
     bool ok = true;
-    if constexpr (LOADER) {
+    if constexpr (PUT) {
       ok = __all_sync(kFull, tc::sleep(raw_full + buf, raw_phase));
-      if (buf == kRawDepth - 1) raw_phase ^= 1;
-      if (ok) put_chunk<MODE, OUTER, A, kStride>(sc, u, lane, raw + buf * kRawBytes,
-                                         m.sf + 512 * group);
+      if (ok) put_chunk<MODE, A, kStride>(sc, u, lane, raw + buf * kRawBytes, m.sf + 512 * group);
       __syncwarp();
-      start(sc, u, buf);
+      if (lane == 0) tc::arrive(m.raw_empty + buf);
     }
+    if (buf == kRawDepth - 1) raw_phase ^= 1;
     asm volatile("bar.sync 1, 128;" ::: "memory");   // the chunk is in its pieces
     // a stage's words are read before the wait for its slot, and the waits
     // spin: the chain from a free slot to its scales in tensor memory bounds
@@ -483,43 +536,42 @@ __device__ __forceinline__ void gemm_scales(const GroupedGemmParams& p, const Ge
   int buf = 0;
   bool ok = true;
   for (GemmWalk<C> w(p, first, step, tiles); ok && !w.done(); w.next()) {
-    int stages = (w.tile(p, m, rank).kb * 32 + C::kStageK - 1) / C::kStageK;
-    for (; ok && stages > 0; stages -= kStagesPerChunk) {
-      const int n = min(stages, kStagesPerChunk);
-      ok = buf == 0 ? serve(src[0], at[0], 0, n) : serve(src[1], at[1], 1, n);
-      buf ^= 1;
+    const GemmTile t = w.tile(p, m, rank);
+    int stages = (t.kb * 32 + C::kStageK - 1) / C::kStageK;
+    ScaleSrc src;
+    if constexpr (PUT) src = scale_src<C>(p, m, t, group);
+    for (int u = 0; ok && stages > 0; stages -= kStagesPerChunk, u += kChunk) {
+      ok = serve(src, u, buf, min(stages, kStagesPerChunk));
+      if (++buf == kRawDepth) buf = 0;
     }
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// The scale warp's role and copies, fixed for the launch.
+// The scale warp's role, fixed for the launch.
 template <typename C>
 __device__ __forceinline__ void gemm_scales_any(const GroupedGemmParams& p, const GemmSmem& m,
-                                                const void* tm_sa, const void* tm_sb,
                                                 uint32_t tbase, int tiles, int first, int step,
                                                 int rank, int group) {
-  const void* tmap = group == 0 ? tm_sa : tm_sb;
-  const bool tiled = group == 0 ? p.a_tiled : p.b_tiled;
-  const int pitch = p.K >> 5;
-#define MOEACT_SCALES(OUTER, MODE, A) \
-  gemm_scales<C, true, OUTER, MODE, A>(p, m, tmap, tbase, tiles, first, step, rank, group)
-#define MOEACT_SCALES_OF(OUTER, A)                             \
+#define MOEACT_SCALES(MODE, A) \
+  gemm_scales<C, true, MODE, A>(p, m, tbase, tiles, first, step, rank, group)
+#define MOEACT_SCALES_OF(OUTER, TILED, A)                      \
   if constexpr (OUTER) {                                       \
-    if (tiled) MOEACT_SCALES(true, kTiled, A);                 \
-    else MOEACT_SCALES(true, kCols, A);                        \
+    if (TILED) MOEACT_SCALES(kTiled, A);                       \
+    else MOEACT_SCALES(kCols, A);                              \
   } else {                                                     \
-    if (tiled) MOEACT_SCALES(false, kTiled, A);                \
-    else if ((pitch & 15) == 0) MOEACT_SCALES(false, kRows16, A); \
-    else if ((pitch & 3) == 0) MOEACT_SCALES(false, kRows4, A);   \
-    else MOEACT_SCALES(false, kRowsAny, A);                    \
+    switch (scale_mode(false, TILED, p.K >> 5)) {              \
+      case kTiled: MOEACT_SCALES(kTiled, A); break;            \
+      case kRows16: MOEACT_SCALES(kRows16, A); break;          \
+      case kFlat: MOEACT_SCALES(kFlat, A); break;              \
+      default: MOEACT_SCALES(kRowsAny, A);                     \
+    }                                                          \
   }
   if (group == 0) {
-    MOEACT_SCALES_OF(C::kAmn, true)
+    MOEACT_SCALES_OF(C::kAmn, p.a_tiled, true)
   } else if (group < C::kGroups) {
-    MOEACT_SCALES_OF(C::kBmn, false)
+    MOEACT_SCALES_OF(C::kBmn, p.b_tiled, false)
   } else {
-    gemm_scales<C, false, false, kRows16, false>(p, m, tmap, tbase, tiles, first, step, rank, 0);
+    gemm_scales<C, false, kRows16, false>(p, m, tbase, tiles, first, step, rank, 0);
   }
 #undef MOEACT_SCALES_OF
 #undef MOEACT_SCALES
@@ -828,7 +880,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   m.full = bars;
   m.empty = m.full + C::kStages;
   m.raw_full = m.empty + C::kStages;
-  m.d_full = m.raw_full + C::kGroups * kRawDepth;
+  m.raw_empty = m.raw_full + C::kGroups * kRawDepth;
+  m.d_full = m.raw_empty + kRawDepth;
   m.d_empty = m.d_full + 2;
   m.misc = reinterpret_cast<int*>(bars + 64);
   m.scan = m.misc + 16;
@@ -899,6 +952,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       mbar_init(m.empty + i, 1);
     }
     for (int i = 0; i < C::kGroups * kRawDepth; ++i) mbar_init(m.raw_full + i, 32);
+    for (int i = 0; i < kRawDepth; ++i) mbar_init(m.raw_empty + i, C::kGroups);
     for (int i = 0; i < 2; ++i) {
       mbar_init(m.d_full + i, 1);
       mbar_init(m.d_empty + i, 4 * C::kCG);
@@ -917,9 +971,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const uint32_t tbase = *reinterpret_cast<volatile uint32_t*>(m.misc);
 
   if (warp < 4) gemm_epilogue<C>(p, m, &tm_out, tbase, tiles, first, step, rank);
-  else if (warp < 8) 
-    gemm_scales_any<C>(p, m, &tm_sa, &tm_sb, tbase, tiles, first, step, rank, warp - 4);
+  else if (warp < 8)  gemm_scales_any<C>(p, m, tbase, tiles, first, step, rank, warp - 4);
   else if (warp == 8) gemm_producer<C>(p, m, &tm_a, &tm_b, tiles, first, step, rank);
+  else if (warp == 10) gemm_scale_loader<C>(p, m, &tm_sa, &tm_sb, tiles, first, step, rank);
   else if (rank == 0) gemm_mma<C>(p, m, tbase, tiles, first, step);
 
   tc::fence_before();
