@@ -521,15 +521,22 @@ def grouped_scaled_swiglu_mxfp8_fc2(x, s, row_offs, w_codes, w_scales, *, status
 
 
 # ------------------------------------------------------------------ plain quantizers
+# (These calls are short next to a small product's few microseconds, so their
+# checks read each tensor attribute once.)
+_U8, _F8, _BF16, _F32 = torch.uint8, torch.float8_e4m3fn, torch.bfloat16, torch.float32
+
+
 def _call_on(dev, name, *args):
     """Calls the library with `dev` current (the tensors' device may be another
     than the current one), on that device's current stream."""
-    stream = ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(dev.index))
-    if torch.cuda.current_device() == dev.index:
-        _capi.call(name, *args, stream)
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        st = getattr(_capi.lib(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(dev):
-            _capi.call(name, *args, stream)
+            st = getattr(_capi.lib(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _capi.check(st, name)
 
 
 def _layout(gemm_scales):
@@ -545,8 +552,9 @@ def _flag(noop_flag, dev):
 
 
 def _offsets(t, name, E, dev):
-    if t.dtype != torch.int64 or t.dim() != 1 or t.device != dev or not t.is_contiguous() or \
-            (E is not None and t.shape[0] != E + 1) or t.shape[0] < 2:
+    shape = t.shape
+    if t.dtype != torch.int64 or len(shape) != 1 or t.device != dev or not t.is_contiguous() or \
+            shape[0] < 2 or (E is not None and shape[0] != E + 1):
         n = "E + 1" if E is None else E + 1
         raise ValueError(f"{name} must be a contiguous int64 vector of {n} offsets on {dev}")
     return t.data_ptr()
@@ -561,11 +569,24 @@ def _status(status, dev):
 
 
 def _row_stride(t):
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    st = t.stride(0)
+    return st if t.shape[0] > 1 else max(st, t.shape[1])
+
+
+_none_cache = {}
+
+
+def _none(dev):
+    """The zero-sized (codes, scales) of a direction that is not asked for."""
+    r = _none_cache.get(dev)
+    if r is None:
+        e = torch.empty(0, dtype=_U8, device=dev)
+        r = _none_cache[dev] = (e.view(_F8), e)
+    return r
 
 
 def _quantize8(x, rowwise, colwise, gemm_scales, noop_flag, out, grouped):
-    _check_rows(x, "x", torch.bfloat16, 0)
+    _check_rows(x, "x", _BF16, 0)
     M, N = x.shape
     dev = x.device
     dirs = _dirs(rowwise, colwise)
@@ -577,20 +598,36 @@ def _quantize8(x, rowwise, colwise, gemm_scales, noop_flag, out, grouped):
         E = row_offs.shape[0] - 1
         ro, cb = _offsets(row_offs, "row_offs", None, dev), _offsets(colblk_offs, "colblk_offs", E, dev)
         col_rows += E
-    take = _alloc_mx(M, N, dirs, dev, col_rows) if out is None else \
-        _take_mx(out, M, N, dirs, dev, col_rows)
-    _flag(noop_flag, dev)
-    if M == 0:
-        if grouped is not None:
-            status.zero_()
-        return _mx_result(*take, view)
-    mx = _mx_struct(*take, dirs, gemm_scales, noop_flag)
-    if grouped is None:
-        _call_on(dev, "mxfp8_quantize", x.data_ptr(), _row_stride(x), M, N, dirs, mx)
+    rq = rs = cq = cs = None
+    if out is None:
+        if rowwise:
+            rq = torch.empty((M, N), dtype=_F8, device=dev)
+            rs = torch.empty((M, N // 32), dtype=_U8, device=dev)
+        if colwise:
+            cq = torch.empty((M, N), dtype=_F8, device=dev)
+            cs = torch.empty((col_rows, N), dtype=_U8, device=dev)
     else:
-        _call_on(dev, "grouped_mxfp8_quantize", x.data_ptr(), _row_stride(x), M, N, dirs, ro, cb, E,
-                 status.data_ptr(), mx)
-    return _mx_result(*take, view)
+        rq, rs, cq, cs = _take_mx(out, M, N, dirs, dev, col_rows)
+        rq, cq = rq.view(_F8), cq.view(_F8)
+    flag = _flag(noop_flag, dev)
+    if M:
+        mx = _capi.MxOut(rq.data_ptr() if rowwise else None, rs.data_ptr() if rowwise else None,
+                         cq.data_ptr() if colwise else None, cs.data_ptr() if colwise else None,
+                         _layout(gemm_scales), flag)
+        if grouped is None:
+            _call_on(dev, "mxfp8_quantize", x.data_ptr(), _row_stride(x), M, N, dirs, mx)
+        else:
+            _call_on(dev, "grouped_mxfp8_quantize", x.data_ptr(), _row_stride(x), M, N, dirs, ro,
+                     cb, E, status.data_ptr(), mx)
+    elif grouped is not None:
+        status.zero_()
+    if not rowwise:
+        rq, rs = _none(dev)
+    if not colwise:
+        cq, cs = _none(dev)
+    elif view is not None:
+        cs = cs[:view]
+    return MXFP8(rq, cq, rs, cs)
 
 
 def mxfp8_quantize(x, *, rowwise=True, colwise=True, gemm_scales=False, noop_flag=None, out=None):
@@ -614,9 +651,10 @@ def _u8(t, name, shape, dev):
     """The pointer of a contiguous uint8 (or E4M3) tensor of this shape."""
     if t is None:
         raise ValueError(f"{name} is required")
-    if t.dtype != torch.uint8 and t.dtype != torch.float8_e4m3fn:
-        raise TypeError(f"{name} must be uint8 or float8_e4m3fn, got {t.dtype}")
-    if t.device != dev or not t.is_contiguous() or tuple(t.shape) != shape:
+    dt = t.dtype
+    if dt != _U8 and dt != _F8:
+        raise TypeError(f"{name} must be uint8 or float8_e4m3fn, got {dt}")
+    if t.shape != shape or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {list(shape)} tensor on {dev}, got "
                          f"{list(t.shape)} on {t.device}")
     return t.data_ptr()
@@ -633,8 +671,8 @@ def mxfp4_quantize(x, *, gemm_scales=False, noop_flag=None, out=None):
     if N % 32 or N == 0:
         raise ValueError(f"x must have a positive multiple of 32 columns, got {N}")
     if out is None:
-        out = MXFP4(torch.empty((M, N // 2), dtype=torch.uint8, device=dev),
-                    torch.empty((M, N // 32), dtype=torch.uint8, device=dev))
+        out = MXFP4(torch.empty((M, N // 2), dtype=_U8, device=dev),
+                    torch.empty((M, N // 32), dtype=_U8, device=dev))
         codes, scales = out.codes.data_ptr(), out.scales.data_ptr()
     else:
         codes = _u8(out.codes, "out.codes", (M, N // 2), dev)
@@ -649,16 +687,15 @@ def mxfp4_quantize(x, *, gemm_scales=False, noop_flag=None, out=None):
 def mxfp4_dequantize(q, *, gemm_scales=False, noop_flag=None, out=None):
     """The bf16 values [M, N] that an MXFP4 stands for.  out: a caller-owned
     bf16 [M, N] tensor with unit column stride."""
-    M, N = q.codes.shape[0], 2 * q.codes.shape[1]
-    dev = q.codes.device
-    if not q.codes.is_cuda:
-        raise ValueError("codes must be a CUDA tensor")
+    shape, dev = q.codes.shape, q.codes.device
+    if dev.type != "cuda" or len(shape) != 2:
+        raise ValueError("codes must be a 2-D CUDA tensor")
+    M, N = shape[0], 2 * shape[1]
     codes = _u8(q.codes, "codes", (M, N // 2), dev)
     scales = _u8(q.scales, "scales", (M, N // 32), dev)
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    elif out.dtype != torch.bfloat16 or tuple(out.shape) != (M, N) or out.stride(1) != 1 or \
-            out.device != dev:
+    elif out.dtype != _BF16 or out.shape != (M, N) or out.stride(1) != 1 or out.device != dev:
         raise ValueError(f"out must be a bf16 [{M}, {N}] tensor with unit column stride on {dev}")
     flag = _flag(noop_flag, dev)
     if M:
@@ -674,9 +711,10 @@ _OUT = {torch.bfloat16: _capi.OUT_BF16, torch.float32: _capi.OUT_FP32}
 def _out_dtype(out_dtype, out):
     if out is not None:
         out_dtype = out.dtype
-    if out_dtype not in _OUT:
+    code = _OUT.get(out_dtype)
+    if code is None:
         raise TypeError(f"the output must be bfloat16 or float32, got {out_dtype}")
-    return out_dtype
+    return out_dtype, code
 
 
 def _product(name, codes, scales, per_byte, w_codes, w_scales, w_inner, row_offs, out_dtype, out,
@@ -686,35 +724,42 @@ def _product(name, codes, scales, per_byte, w_codes, w_scales, w_inner, row_offs
     if codes is None or scales is None or w_codes is None or w_scales is None:
         raise ValueError("codes and scales of both operands are required, "
                          + ("rowwise" if w_inner else "rowwise of dy and colwise of w"))
-    if not codes.is_cuda or codes.dim() != 2:
+    shape, dev = codes.shape, codes.device
+    if len(shape) != 2 or dev.type != "cuda":
         raise ValueError("the rows' codes must be a 2-D CUDA tensor")
-    dev = codes.device
-    M, K = codes.shape[0], codes.shape[1] * per_byte
+    M, bytes_ = shape
+    K = bytes_ * per_byte
     E = row_offs.shape[0] - 1
     ro = _offsets(row_offs, "row_offs", None, dev)
-    if w_codes.dim() == 3:
+    w_shape = w_codes.shape
+    if len(w_shape) == 3:
         w_codes, w_scales = w_codes.flatten(0, 1), w_scales.flatten(0, 1)
-    rows, width = w_codes.shape
-    if rows % E or (width * per_byte if w_inner else rows // E) != K:
-        raise ValueError(f"w of shape {list(w_codes.shape)} does not hold {E} matrices for rows of "
-                         f"{K} values")
+        w_shape = w_codes.shape
+    if len(w_shape) != 2:
+        raise ValueError("w must be [E * H, K] or [E, H, K]")
+    rows, width = w_shape
     N = rows // E if w_inner else width
-    a, sa = _u8(codes, "codes", (M, K // per_byte), dev), _u8(scales, "scales", (M, K // 32), dev)
+    if rows % E or (width * per_byte if w_inner else rows // E) != K:
+        raise ValueError(f"w of shape {list(w_shape)} does not hold {E} matrices for rows of "
+                         f"{K} values")
+    a, sa = _u8(codes, "codes", (M, bytes_), dev), _u8(scales, "scales", (M, K // 32), dev)
     w = _u8(w_codes, "w codes", (rows, width), dev)
     sw = _u8(w_scales, "w scales", (rows, K // 32) if w_inner else (rows // 32, width), dev)
-    dt = _out_dtype(out_dtype, out)
+    dt, code = _out_dtype(out_dtype, out)
     if out is None:
         out = torch.empty((M, N), dtype=dt, device=dev)
-    elif out.dim() != 2 or out.shape[0] != M or out.shape[1] != N or out.stride(1) != 1 or \
-            out.device != dev:
-        raise ValueError(f"out must be a [{M}, {N}] tensor with unit column stride on {dev}")
+        stride = N
+    else:
+        if out.shape != (M, N) or out.stride(1) != 1 or out.device != dev:
+            raise ValueError(f"out must be a [{M}, {N}] tensor with unit column stride on {dev}")
+        stride = _row_stride(out)
     status = _status(status, dev)
     flag = _flag(noop_flag, dev)
     if M == 0:
         status.zero_()
         return out, status
     _call_on(dev, name, a, sa, _layout(a_gemm), M, K, ro, E, status.data_ptr(), w, sw,
-             _layout(w_gemm), N, out.data_ptr(), _row_stride(out), _OUT[dt], flag)
+             _layout(w_gemm), N, out.data_ptr(), stride, code, flag)
     return out, status
 
 
@@ -756,32 +801,33 @@ def grouped_mxfp8_wgrad(dy, x, row_offs, colblk_offs, *, out_dtype=torch.float32
     if dy.col_codes is None or x.col_codes is None or dy.col_scales is None or x.col_scales is None:
         raise ValueError("colwise codes and scales of dy and x are required")
     cy, cx = dy.col_codes, x.col_codes
-    if not cy.is_cuda or cy.dim() != 2 or cx.dim() != 2:
-        raise ValueError("dy and x codes must be 2-D CUDA tensors")
     dev = cy.device
+    if dev.type != "cuda" or cy.dim() != 2 or cx.dim() != 2:
+        raise ValueError("dy and x codes must be 2-D CUDA tensors")
     (M, H), K = cy.shape, cx.shape[1]
     E = row_offs.shape[0] - 1
     ro, cb = _offsets(row_offs, "row_offs", None, dev), _offsets(colblk_offs, "colblk_offs", E, dev)
     pc, px = _u8(cy, "dy codes", (M, H), dev), _u8(cx, "x codes", (M, K), dev)
+    ptrs, rows = [], None
     for t, name, width in ((dy.col_scales, "dy scales", H), (x.col_scales, "x scales", K)):
         # the exact number of scale rows, sum ceil(m_e / 32), is on the device;
         # it is at least ceil(M / 32)
-        if t.dim() != 2 or t.shape[0] < (M + 31) // 32:
+        n = t.shape[0] if t.dim() == 2 else -1
+        if n < (M + 31) // 32:
             raise ValueError(f"{name} must have the sum of ceil(m_e / 32) rows")
-        _u8(t, name, (t.shape[0], width), dev)
-    rows = min(dy.col_scales.shape[0], x.col_scales.shape[0])
-    dt = _out_dtype(out_dtype, out)
+        ptrs.append(_u8(t, name, (n, width), dev))
+        rows = n if rows is None else min(rows, n)
+    dt, code = _out_dtype(out_dtype, out)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    if accumulate and dt != torch.float32:
+    if accumulate and dt != _F32:
         raise TypeError("accumulate needs a float32 out")
     if out is None:
         out = torch.empty((E, H, K), dtype=dt, device=dev)
-    elif tuple(out.shape) != (E, H, K) or not out.is_contiguous() or out.device != dev:
+    elif out.shape != (E, H, K) or not out.is_contiguous() or out.device != dev:
         raise ValueError(f"out must be a contiguous [{E}, {H}, {K}] tensor on {dev}")
     status = _status(status, dev)
     flag = _flag(noop_flag, dev)
-    _call_on(dev, "grouped_mxfp8_wgrad", pc, dy.col_scales.data_ptr(), px, x.col_scales.data_ptr(),
-             rows, _layout(gemm_scales), M, H, K, ro, cb, E, status.data_ptr(), out.data_ptr(),
-             _OUT[dt], int(bool(accumulate)), flag)
+    _call_on(dev, "grouped_mxfp8_wgrad", pc, ptrs[0], px, ptrs[1], rows, _layout(gemm_scales), M, H,
+             K, ro, cb, E, status.data_ptr(), out.data_ptr(), code, 1 if accumulate else 0, flag)
     return out, status
