@@ -17,7 +17,7 @@
 #include "fc2.cuh"
 #include "grouped_gemm.cuh"
 #include "host_kernels.cuh"
-#include "mxfp4.cuh"
+#include "mx_rows.cuh"
 #include "variants.cuh"
 
 namespace moeact {
@@ -563,6 +563,27 @@ moeact_status fwd_common(const ActArgs& a, const void* x, int64_t ldx, const flo
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   int dev;
   if ((st = ensure_ready(cs, &dev))) return st;
+  if (act == kPlain && dirs == MOEACT_ROWWISE) {
+    // a kernel without tiles of 32 rows: a single row is spread over the SMs
+    MxRowsParams r{};
+    r.x = static_cast<uint16_t*>(const_cast<void*>(x));
+    r.ldx = ldx;
+    r.M = M;
+    r.K = (int)N;
+    r.codes = out.row_codes;
+    r.scales = out.row_scales;
+    r.tiled = out.scale_layout == MOEACT_SCALES_GEMM;
+    r.row_offs = ro;
+    r.cb_offs = cb;
+    r.E = grouped ? E : 0;
+    r.status = status;
+    r.noop = out.noop_flag;
+    if (ceil_div(M, 4) * ceil_div(N, 256) > INT32_MAX)
+      return fail(MOEACT_ERANGE, "more than 2^31 - 1 pieces of 4 rows x 256 columns");
+    const cudaError_t e = mxfp8_rows_launch(r, g_sms[dev], cs);
+    if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
+    return MOEACT_OK;
+  }
   Params p{};
   p.x = static_cast<const uint16_t*>(x);
   p.ldx = ldx;
@@ -726,7 +747,7 @@ moeact_status mxfp4_common(const void* x, int64_t ldx, int64_t M, int64_t N, voi
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   int dev;
   if ((st = ensure_ready(cs, &dev))) return st;
-  Mxfp4Params p{};
+  MxRowsParams p{};
   p.x = static_cast<uint16_t*>(const_cast<void*>(x));
   p.ldx = ldx;
   p.M = M;
@@ -736,7 +757,7 @@ moeact_status mxfp4_common(const void* x, int64_t ldx, int64_t M, int64_t N, voi
   p.tiled = layout == MOEACT_SCALES_GEMM;
   p.noop = noop;
   const cudaError_t e = back ? mxfp4_dequantize_launch(p, g_sms[dev], cs)
-                             : mxfp4_quantize_launch(p, g_sms[dev], cs);
+                             : mxfp4_rows_launch(p, g_sms[dev], cs);
   if (e != cudaSuccess) return cuda_fail(e, "MXFP4 launch");
   return MOEACT_OK;
 }
@@ -1234,8 +1255,6 @@ moeact_status grouped_mxfp8_wgrad(const void* dy_codes, const void* dy_scales,
   p.E = num_groups;
   p.R = (int)H;
   p.N = (int)K;
-  p.a_codes = static_cast<const uint8_t*>(dy_codes);
-  p.b_codes = static_cast<const uint8_t*>(x_codes);
   p.a_scales = static_cast<const uint8_t*>(dy_scales);
   p.b_scales = static_cast<const uint8_t*>(x_scales);
   p.a_tiled = p.b_tiled = scale_layout == MOEACT_SCALES_GEMM;

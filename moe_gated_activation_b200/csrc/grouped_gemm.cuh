@@ -27,8 +27,6 @@ struct GroupedGemmParams {
   int K;                      // forward, dgrad: length of the summed index (multiple of 32)
   int R;                      // wgrad: rows of dW_e (A's columns)
   int N;                      // output columns
-  const uint8_t* a_codes;     // wgrad only: row tails are read with plain loads
-  const uint8_t* b_codes;
   const uint8_t* a_scales;
   const uint8_t* b_scales;
   int a_tiled, b_tiled;       // scale layouts: 0 row-major, 1 tiles of 128 x 4
@@ -41,7 +39,6 @@ struct GroupedGemmParams {
   uint32_t* err;              // device error word
 };
 
-constexpr int kGemmThreads = 352;   // 4 epilogue, 4 scale, a TMA, an MMA and a scale-loading warp
 // Rows of a tensor-map box: 128 (an SM's share of an operand tile), except 32
 // where fewer rows may be wanted: the A rows of the one-SM kernels, whose
 // groups can be short, and operands stored with the summed index outermost,

@@ -14,6 +14,7 @@
 //   warps 4-7  scales: E8M0 words from shared memory, as they came, into the
 //              order of tensor memory and each stage's there (tcgen05.st);
 //   warp 10    the scales' copies into shared memory, some chunks ahead;
+//   warp 11    wgrad: clears the rows past a group's end;
 //   warp 8     TMA loads of the code tiles (128 rows x 128 bytes each);
 //   warp 9     tensor-memory allocation; in the pair's first SM the MMAs.
 // One ring of stages carries codes and scales: `full` collects the TMA bytes
@@ -50,6 +51,7 @@ struct GemmCfg {
   static constexpr bool kWgrad = OP == kGemmWgrad;
   static constexpr bool kAmn = OP == kGemmWgrad;                      // A rows = summed index
   static constexpr bool kBmn = OP == kGemmWgrad || OP == kGemmDgrad;  // B rows = summed index
+  static constexpr int kThreads = kWgrad ? 384 : 352;
   static constexpr int kCG = PAIR ? 2 : 1;
   static constexpr int kTM = 128 * kCG;
   static constexpr int kBN = PAIR ? 256 : 128;
@@ -83,13 +85,14 @@ struct GemmSmem {
   unsigned char* sf;   // [kChunk][A's rows, B's rows by 128][512] scale words
   unsigned char* raw;  // [groups][kRawDepth][kRawBytes] the same as they arrive
   uint64_t* full;      // [kStages] (first SM of a pair) codes and scales are in
+  uint64_t* landed;    // [kStages] wgrad: this SM's codes are in, group ends not yet cleared
   uint64_t* empty;     // [kStages] the stage's MMAs are done
   uint64_t* raw_full;  // [groups][kRawDepth] a chunk of scales has arrived
   uint64_t* raw_empty; // [kRawDepth] ... and is in its pieces
   uint64_t* d_full;    // [2] an accumulator holds a finished tile
   uint64_t* d_empty;   // [2] (first SM) its columns may be overwritten
   int* misc;           // [0] tensor-memory base, [1] abort
-  int* scan;           // [11] warp totals
+  int* scan;           // [12] warp totals
   int* ro;             // [E + 1] the row offsets (below 2^30)
   int* pre;            // [E + 1] row tiles before each expert; wgrad: scale rows before it
 };
@@ -578,27 +581,10 @@ __device__ __forceinline__ void gemm_scales_any(const GroupedGemmParams& p, cons
 }
 
 // ------------------------------------------------------------ code tiles
-// Warp 8.  wgrad: the last rows of a group, when they are no multiple of 32,
-// are copied with plain loads and zeros after them, for both operands (rows of
-// the next group must not meet in the sum, and zeros times its NaNs would
-// not be zero).
-template <typename C>
-__device__ __forceinline__ void copy_tail(unsigned char* dst, const uint8_t* src, int64_t ld,
-                                          int64_t row, int rows, int col, int lane) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = 4 * i + (lane >> 3), c = lane & 7;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (r < rows && col + 16 * c < ld)
-      v = __ldg(reinterpret_cast<const uint4*>(src + (row + r) * ld + col + 16 * c));
-    *reinterpret_cast<uint4*>(dst + r * 128 + ((c ^ (r & 7)) << 4)) = v;
-  }
-}
-
+// Warp 8.
 template <typename C>
 __device__ void gemm_producer(const GroupedGemmParams& p, const GemmSmem& m, const void* tm_a,
                               const void* tm_b, int tiles, int first, int step, int rank) {
-  const int lane = threadIdx.x & 31;
   const bool leader = tc::elect_one();
   int slot = 0;
   uint32_t phase = 1;
@@ -613,36 +599,31 @@ __device__ void gemm_producer(const GroupedGemmParams& p, const GemmSmem& m, con
       }
       unsigned char* da = m.stages + slot * C::kStageBytes;
       unsigned char* db = da + kTileBytes;
-      const uint32_t bar = tc::leader_addr(m.full + slot);
+      // wgrad's copies complete on a barrier of this SM's: gemm_clear passes
+      // them on
+      const uint32_t bar = C::kAmn ? smem_addr(m.landed + slot) : tc::leader_addr(m.full + slot);
       int na = 0, nb = 1;   // boxes of A and B
       if constexpr (C::kAmn) {
-        const int left = tile.krows - 128 * s, full = min(4, left >> 5);
-        na = nb = full;
-        if (full < 4 && (left & 31) != 0) {
-          copy_tail<C>(da + full * 4096, p.a_codes, p.R, tile.k0 + 128 * s + 32 * full, left & 31,
-                       (int)tile.row0, lane);
-          copy_tail<C>(db + full * 4096, p.b_codes, p.N, tile.k0 + 128 * s + 32 * full, left & 31,
-                       col_b, lane);
-          tc::fence_proxy_async();
-        }
+        na = nb = min(4, tile.kb - 4 * s);
       } else {
         na = (tile.rows + C::kABox - 1) / C::kABox;
         if constexpr (C::kBmn) nb = min(4, tile.kb - 4 * s);
       }
-      __syncwarp();
       if (leader) {
-        tc::arrive_tx_cluster(bar, (uint32_t)(na * C::kABox + nb * C::kBBox) * 128u);
+        const uint32_t bytes = (uint32_t)(na * C::kABox + nb * C::kBBox) * 128u;
+        if constexpr (C::kAmn) mbar_expect_tx(m.landed + slot, bytes);
+        else tc::arrive_tx_cluster(bar, bytes);
         for (int i = 0; i < na; ++i) {
           if constexpr (C::kAmn)
-            tc::load_2d<C::kCG>(da + i * 4096, tm_a, (int)tile.row0,
-                                (int)tile.k0 + 128 * s + 32 * i, bar);
+            tc::load_2d<1>(da + i * 4096, tm_a, (int)tile.row0, (int)tile.k0 + 128 * s + 32 * i,
+                           bar);
           else
             tc::load_2d<C::kCG>(da + i * C::kABox * 128, tm_a, 128 * s,
                                 (int)tile.row0 + C::kABox * i, bar);
         }
         for (int i = 0; i < nb; ++i) {
           if constexpr (C::kAmn)
-            tc::load_2d<C::kCG>(db + i * 4096, tm_b, col_b, (int)tile.k0 + 128 * s + 32 * i, bar);
+            tc::load_2d<1>(db + i * 4096, tm_b, col_b, (int)tile.k0 + 128 * s + 32 * i, bar);
           else if constexpr (C::kBmn)
             tc::load_2d<C::kCG>(db + i * 4096, tm_b, col_b, tile.e * p.K + 128 * s + 32 * i, bar);
           else
@@ -650,6 +631,39 @@ __device__ void gemm_producer(const GroupedGemmParams& p, const GemmSmem& m, con
         }
       }
       __syncwarp();
+      if (++slot == C::kStages) slot = 0, phase ^= 1;
+    }
+  }
+}
+
+// Warp 11, wgrad: once a stage has landed, clears the rows past the group's end
+// in its last block of 32 -- in both operands: the next group's rows must not
+// meet in the sum, and a zero times a NaN of theirs would not be zero -- and
+// passes the stage on to the MMAs.
+template <typename C>
+__device__ void gemm_clear(const GroupedGemmParams& p, const GemmSmem& m, int tiles, int first,
+                           int step, int rank) {
+  const int lane = threadIdx.x & 31;
+  int slot = 0;
+  uint32_t phase = 0;
+  for (GemmWalk<C> walk(p, first, step, tiles); !walk.done(); walk.next()) {
+    const GemmTile tile = walk.tile(p, m, rank);
+    for (int left = tile.krows; left > 0; left -= 128) {
+      if (!__all_sync(kFull, tc::spin(m.landed + slot, phase))) {
+        gemm_abort(p, m);
+        return;
+      }
+      if (left < 128 && (left & 31) != 0) {
+        unsigned char* a = m.stages + slot * C::kStageBytes + left * 128;
+        const int n = (32 - (left & 31)) * 8;   // 16-byte pieces
+        for (int i = lane; i < n; i += 32) {
+          reinterpret_cast<uint4*>(a)[i] = make_uint4(0u, 0u, 0u, 0u);
+          reinterpret_cast<uint4*>(a + kTileBytes)[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        tc::fence_proxy_async();
+      }
+      __syncwarp();
+      if (lane == 0) tc::arrive_cluster(tc::leader_addr(m.full + slot));
       if (++slot == C::kStages) slot = 0, phase ^= 1;
     }
   }
@@ -823,6 +837,8 @@ __device__ void gemm_epilogue(const GroupedGemmParams& p, const GemmSmem& m, con
       tc::ld32(src + 64 * c, v);
       tc::ld32(src + 64 * c + 32, v + 32);
       tc::wait_ld();
+      tc::tie(v);
+      tc::tie(v + 32);
       if (i == (kOver ? kOver : kChunks) - 1) {
         tc::fence_before();
         __syncwarp();
@@ -861,7 +877,7 @@ __device__ void gemm_epilogue(const GroupedGemmParams& p, const GemmSmem& m, con
 
 // ------------------------------------------------------------ kernel
 template <int OP, bool PAIR>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(GemmCfg<OP, PAIR>::kThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
                         const __grid_constant__ CUtensorMap tm_b,
                         const __grid_constant__ CUtensorMap tm_sa,
@@ -878,7 +894,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   m.raw = m.sf + C::kSfBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(m.raw + C::kGroups * C::kRawGroupBytes);
   m.full = bars;
-  m.empty = m.full + C::kStages;
+  m.landed = m.full + C::kStages;
+  m.empty = m.landed + C::kStages;
   m.raw_full = m.empty + C::kStages;
   m.raw_empty = m.raw_full + C::kGroups * kRawDepth;
   m.d_full = m.raw_empty + kRawDepth;
@@ -899,7 +916,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
   // ---- the groups: offsets checked, row tiles before each expert
   const int E = p.E;
-  const int per = (E + kGemmThreads - 1) / kGemmThreads;
+  const int per = (E + C::kThreads - 1) / C::kThreads;
   const int e_lo = min(E, tid * per), e_hi = min(E, e_lo + per);
   int local = 0, bad = 0;
   for (int e = e_lo; e < e_hi; ++e) {
@@ -928,7 +945,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   if (blockIdx.x == 0 && tid == 0) *p.status = bad1 ? 3 : bad2 ? 4 : 0;
   if (bad1 || bad2) return;
   int before = incl - local, total = 0;
-  for (int w = 0; w < kGemmThreads / 32; ++w) {
+  for (int w = 0; w < C::kThreads / 32; ++w) {
     const int v = m.scan[w];
     if (w < warp) before += v;
     total += v;
@@ -948,7 +965,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   // ---- barriers and tensor memory
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(m.full + i, 5 * C::kCG);   // per SM: the TMA warp and four scale warps
+      mbar_init(m.full + i, 5 * C::kCG);   // per SM: warp 8 (wgrad: 11) and four scale warps
+      mbar_init(m.landed + i, 1);
       mbar_init(m.empty + i, 1);
     }
     for (int i = 0; i < C::kGroups * kRawDepth; ++i) mbar_init(m.raw_full + i, 32);
@@ -974,6 +992,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   else if (warp < 8)  gemm_scales_any<C>(p, m, tbase, tiles, first, step, rank, warp - 4);
   else if (warp == 8) gemm_producer<C>(p, m, &tm_a, &tm_b, tiles, first, step, rank);
   else if (warp == 10) gemm_scale_loader<C>(p, m, &tm_sa, &tm_sb, tiles, first, step, rank);
+  else if (C::kWgrad && warp == 11) gemm_clear<C>(p, m, tiles, first, step, rank);
   else if (rank == 0) gemm_mma<C>(p, m, tbase, tiles, first, step);
 
   tc::fence_before();
@@ -1017,7 +1036,7 @@ cudaError_t gemm_launch_one(const GroupedGemmParams& p, const GemmMaps& tm, int 
   const int64_t most = n_sms / C::kCG;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * C::kCG));
-  cfg.blockDim = dim3(kGemmThreads);
+  cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = gemm_smem_bytes<OP, PAIR>(p.E);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];

@@ -45,11 +45,14 @@ void put_bwd(BwdVariant* t) {
 template <int ACT, bool STAGED, bool GROUPED, bool ILV = false>
 void fill_fwd(FwdVariant* t) {
   constexpr int I = ILV ? kIlv : 0;
+  // (rowwise only, the plain quantizer has kernels of its own: mx_rows.cuh)
 #define MOEACT_FWD_DIRS(ST, G)                              \
-  put_fwd<ACT, I | kRow, ST, G>(t);                         \
+  if constexpr (ACT != kPlain) {                            \
+    put_fwd<ACT, I | kRow, ST, G>(t);                       \
+    put_fwd<ACT, I | kRow | kGemm, ST, G>(t);               \
+  }                                                         \
   put_fwd<ACT, I | kCol, ST, G>(t);                         \
   put_fwd<ACT, I | kRow | kCol, ST, G>(t);                  \
-  put_fwd<ACT, I | kRow | kGemm, ST, G>(t);                 \
   put_fwd<ACT, I | kCol | kGemm, ST, G>(t);                 \
   put_fwd<ACT, I | kRow | kCol | kGemm, ST, G>(t);
   MOEACT_FWD_DIRS(false, GROUPED)
