@@ -178,6 +178,45 @@ def test_mxfp8_tiled_and_strided(cuda_device):
     assert torch.equal(q.col_scales, ref.tile_col_scales(p.col_scales, [m // 32 for m in splits]))
 
 
+@pytest.mark.parametrize("M,N", SIZES)
+def test_mxfp8_rowwise_only(cuda_device, M, N):
+    """Rowwise alone: the bits of both directions' rowwise half, dense, grouped,
+    strided, under a no-op flag, and nothing at all for bad offsets."""
+    x = _values(M, N, 6)
+    c, s = _quantize8(x, 1)
+    wide = torch.zeros(M, N + 24, dtype=torch.bfloat16, device="cuda")
+    wide[:, 8:8 + N] = x
+    E = min(M, 5)
+    ro, cb, _ = mg.splits_to_offsets(torch.tensor([M - E + 1] + [1] * (E - 1), device="cuda"), M)
+    for v in (x, wide[:, 8:8 + N]):
+        for q in (mg.mxfp8_quantize(v, colwise=False),
+                  mg.grouped_mxfp8_quantize(v, ro, cb, colwise=False)[0]):
+            assert torch.equal(q.row_codes.view(torch.uint8), c) and torch.equal(q.row_scales, s)
+            assert q.col_codes.numel() == 0 and q.col_scales.numel() == 0
+    held = mg.MXFP8(torch.full_like(c, 9), None, torch.full_like(s, 9), None)
+    on = torch.ones(1, dtype=torch.int32, device="cuda")
+    st = torch.full((1,), 99, dtype=torch.int32, device="cuda")
+    mg.grouped_mxfp8_quantize(x, ro, cb, colwise=False, out=held, noop_flag=on, status=st)
+    assert int(st) == 99 and bool((held.row_codes == 9).all()) and bool((held.row_scales == 9).all())
+    bad = ro.clone()
+    bad[-1] += 1
+    mg.grouped_mxfp8_quantize(x, bad, cb, colwise=False, out=held, status=st)
+    assert int(st) == 3 and bool((held.row_codes == 9).all()) and bool((held.row_scales == 9).all())
+
+
+def test_mxfp8_rowwise_only_tiled(cuda_device):
+    splits, N = [128, 0, 256], 384
+    x = _values(sum(splits), N, 7)
+    c, s = _quantize8(x, 1)
+    ro, cb, _ = mg.splits_to_offsets(torch.tensor(splits, device="cuda"), sum(splits))
+    q, st = mg.grouped_mxfp8_quantize(x, ro, cb, colwise=False, gemm_scales=True)
+    assert int(st) == 0 and torch.equal(q.row_scales, ref.tile_scales(s))
+    assert torch.equal(q.row_codes.view(torch.uint8), c)
+    ro2, cb2, _ = mg.splits_to_offsets(torch.tensor([64, 320], device="cuda"), 384)
+    _, st = mg.grouped_mxfp8_quantize(x, ro2, cb2, colwise=False, gemm_scales=True)
+    assert int(st) == 4
+
+
 def test_no_rows(cuda_device):
     x = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
     assert mg.mxfp8_quantize(x).row_codes.shape == (0, 64)
