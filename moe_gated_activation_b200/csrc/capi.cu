@@ -777,9 +777,14 @@ moeact_status check_gemm_common(int64_t M, const int64_t* ro, int32_t E, int32_t
 }
 
 // Whether a product runs on SM pairs (256 x 256 tiles) or on single SMs (128 x
-// 128): pairs where the rows fill their tiles and the tiles fill the pairs.
-bool gemm_pair(int64_t row_tiles, int64_t col_tiles, int64_t rows_per_group, int dev) {
-  return rows_per_group >= 128 && row_tiles * col_tiles >= g_sms[dev] / 2;
+// 128).  Single SMs where a group's rows fill half a pair's tile at most, or
+// where the small tiles fit the SMs at once.  Measured, pair and single: 32
+// groups of 128 rows into 2048 of 2048: 42.2 and 38.3 us, of 192 rows 43.3 and
+// 47.7; one group of 1024 rows (128 small tiles) 13.9 and 12.2, of 2048 (256)
+// 14.8 and 17.8; wgrad of 8 x 512 x 512 (128) 9.0 and 7.5, of 64 x 256 x 256
+// (256) 9.4 and 9.8.
+bool gemm_pair(int64_t rows_per_group, int64_t small_tiles, int dev) {
+  return rows_per_group > 128 && small_tiles > g_sms[dev];
 }
 
 // Forward and dgrad: rows of A [M, K] times each group's W, rows of K
@@ -833,17 +838,18 @@ moeact_status gemm_rows(int op, const void* a_codes, const void* a_scales, int32
   p.status = status;
   p.noop = noop;
   p.err = g_err_ptr[dev];
-  const bool pair = gemm_pair(ceil_div(M, 256), ceil_div(N, 256), M / E, dev);
+  const bool pair = gemm_pair(M / E, std::max<int64_t>(ceil_div(M, 128), std::min<int64_t>(E, M)) *
+                                         ceil_div(N, 128), dev);
   const int64_t row_bytes = op == kGemmFwd4 ? K / 2 : K;
-  const int a_box = pair ? kGemmBoxRows : kGemmShortBoxRows;
+  const int box = pair ? kGemmBoxRows : kGemmShortBoxRows;
   GemmMaps tm{};
-  if ((st = make_code_map(&tm.a, a_codes, row_bytes, M, a_box))) return st;
+  if ((st = make_code_map(&tm.a, a_codes, row_bytes, M, box))) return st;
   if (dgrad) st = make_code_map(&tm.b, w_codes, N, wrows, kGemmShortBoxRows);
   else st = make_code_map(&tm.b, w_codes, row_bytes, wrows, kGemmBoxRows);
   if (st) return st;
   const int64_t pitch = K / 32;
   if (!p.a_tiled && pitch % 16 == 0 &&
-      (st = make_byte_map(&tm.sa, a_scales, pitch, M, kGemmScaleBytes, a_box)))
+      (st = make_byte_map(&tm.sa, a_scales, pitch, M, kGemmScaleBytes, box)))
     return st;
   if (!p.b_tiled) {
     if (dgrad) st = make_byte_map(&tm.sb, w_scales, N, wrows / 32, 128, 32);
@@ -1275,7 +1281,7 @@ moeact_status grouped_mxfp8_wgrad(const void* dy_codes, const void* dy_scales,
       if ((st = make_byte_map(&tm.sb, x_scales, K, rows, 128, 32))) return st;
     }
   }
-  const bool pair = gemm_pair(num_groups * ceil_div(H, 256), ceil_div(K, 256), H, dev);
+  const bool pair = gemm_pair(H, num_groups * ceil_div(H, 128) * ceil_div(K, 128), dev);
   if ((st = make_out_map(&tm.out, dw, p.out32, K, H, K, num_groups))) return st;
   const cudaError_t e = grouped_gemm_launch(kGemmWgrad, pair, p, tm, g_sms[dev], cs);
   if (e != cudaSuccess) return cuda_fail(e, "grouped product launch");

@@ -91,6 +91,7 @@ struct GemmSmem {
   uint64_t* raw_empty; // [kRawDepth] ... and is in its pieces
   uint64_t* d_full;    // [2] an accumulator holds a finished tile
   uint64_t* d_empty;   // [2] (first SM) its columns may be overwritten
+  int* head;           // [kRawDepth][4] of a raw chunk: its stages, the groups' places (ScaleHead)
   int* misc;           // [0] tensor-memory base, [1] abort
   int* scan;           // [12] warp totals
   int* ro;             // [E + 1] the row offsets (below 2^30)
@@ -117,6 +118,9 @@ struct GemmTile {
 };
 
 // Walks the tiles first, first + step, ...: columns fastest, then rows.
+// (Splitting the tiles of a last, partial wave by columns over idle SMs cost the
+// copying thread more in every stage than the shorter wave gave: 64 rows on 50
+// experts, 2048 -> 1536, 36.9 -> 40 us.)
 template <typename C>
 struct GemmWalk {
   int t, tiles, step;
@@ -348,9 +352,9 @@ __device__ __forceinline__ void put_cols(unsigned char* dst, int lane, uint32_t 
 
 // A chunk that has arrived: its words into the warp's pieces.
 template <int MODE, bool A, int STRIDE>
-__device__ __forceinline__ void put_chunk(const ScaleSrc& c, int u, int lane,
-                                          const unsigned char* raw, unsigned char* sf) {
-  const int n = min(kChunk, c.words - u);
+__device__ __forceinline__ void put_chunk(int head, int pitch, int lane, const unsigned char* raw,
+                                          unsigned char* sf) {
+  const int n = head & 15, first = (head >> 4) & 15, left = (head >> 8) & 63;
   if constexpr (MODE == kTiled) {
     for (int i = 0; i < n; ++i) {
       const uint4 v = *reinterpret_cast<const uint4*>(raw + 512 * i + 16 * lane);
@@ -366,8 +370,7 @@ __device__ __forceinline__ void put_chunk(const ScaleSrc& c, int u, int lane,
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int r = 32 * j + lane;
-      at[j] = MODE == kFlat ? (int)(c.r0 * c.pitch & 15) + r * c.pitch
-                            : 36 * r + (int)((c.r0 + r) * c.pitch & 3);
+      at[j] = MODE == kFlat ? first + r * pitch : 36 * r + ((first + r * pitch) & 3);
       sh[j] = 8 * (at[j] & 3);
       at[j] >>= 2;
     }
@@ -375,7 +378,7 @@ __device__ __forceinline__ void put_chunk(const ScaleSrc& c, int u, int lane,
     for (int i = 0; i < n; ++i) {
       // bytes past the row's end are another row's: a NaN scale there would
       // meet the zeros of half an E2M1 step
-      const int have = min(4, c.pitch - 4 * (u + i));
+      const int have = min(4, left - 4 * i);
       const uint32_t mask = have < 4 ? (1u << (8 * have)) - 1u : ~0u;
       uint32_t w[4];
 #pragma unroll
@@ -408,7 +411,17 @@ __device__ __forceinline__ int scale_mode(bool outer, bool tiled, int pitch) {
          : (pitch & 3) == 0 ? kRows4 : kRowsAny;
 }
 
-// Warp 10: the copies of every chunk of every group, kRawDepth ahead.  (In a
+// What put_chunk needs of a chunk of a group: its words (4 bits), the place of
+// its first byte in the 16 or 4 bytes copied first (4 bits), the bytes of a row
+// left from its first word on (kRowsAny, kFlat; at most 63).
+template <typename C>
+__device__ __forceinline__ int scale_head(const ScaleSrc& c, int u) {
+  const int n = c.n > 0 ? min(kChunk, c.words - u) : 0;
+  return n | ((int)(c.r0 * c.pitch & 15) << 4) | (min(63, c.pitch - 4 * u) << 8);
+}
+
+// Warp 10: the copies of every chunk of every group, kRawDepth ahead, with what
+// the warps that take them need to know (so that they look up no tile).  (In a
 // warp of its own: the setting up of a tile's copies -- a search for the
 // group, 64-bit addresses, cold code -- took one to three thousand cycles out
 // of the warps that feed tensor memory.)
@@ -429,9 +442,13 @@ __device__ void gemm_scale_loader(const GroupedGemmParams& p, const GemmSmem& m,
         gemm_abort(p, m);
         return;
       }
+      if (lane == 0)
+        m.head[4 * buf] = min(kChunk / C::kWords, (t.kb * 32 + C::kStageK - 1) / C::kStageK -
+                                                      u / C::kWords);
 #pragma unroll 1
       for (int g = 0; g < C::kGroups; ++g) {
         const ScaleSrc src = scale_src<C>(p, m, t, g);
+        if (lane == 0) m.head[4 * buf + 1 + g] = scale_head<C>(src, u);
         unsigned char* raw = m.raw + g * C::kRawGroupBytes + buf * kRawBytes;
         uint64_t* bar = m.raw_full + g * kRawDepth + buf;
         const int mode = g == 0 ? mode_a : mode_b;
@@ -458,6 +475,13 @@ __device__ void gemm_scale_loader(const GroupedGemmParams& p, const GemmSmem& m,
       if (++buf == kRawDepth) buf = 0, phase ^= 1;
     }
   }
+  // the end: a chunk without stages
+  if (!__all_sync(kFull, tc::sleep(m.raw_empty + buf, phase)) || gemm_aborted(m)) {
+    gemm_abort(p, m);
+    return;
+  }
+  if (lane == 0) m.head[4 * buf] = 0;
+  for (int g = 0; g < C::kGroups; ++g) tc::arrive(m.raw_full + g * kRawDepth + buf);
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
@@ -467,8 +491,7 @@ __device__ void gemm_scale_loader(const GroupedGemmParams& p, const GemmSmem& m,
 // quarter.
 template <typename C, bool PUT, int MODE, bool A>
 __device__ __forceinline__ void gemm_scales(const GroupedGemmParams& p, const GemmSmem& m,
-                                            uint32_t tbase, int tiles, int first, int step,
-                                            int rank, int group) {
+                                            uint32_t tbase, int group) {
   const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3;
   const uint32_t dst0 = tbase + ((uint32_t)(32 * q) << 16) + (uint32_t)C::kSfCol;
   const uint32_t full0 = tc::leader_addr(m.full);
@@ -479,14 +502,19 @@ __device__ __forceinline__ void gemm_scales(const GroupedGemmParams& p, const Ge
   int slot = 0;
   uint32_t phase = 1;   // a fresh barrier's preceding phase counts as complete
   uint32_t raw_phase = 0;
-  auto serve = [&](const ScaleSrc& sc, int u, int buf, int stages) {
-    bool ok = true;
-    if constexpr (PUT) {
-      ok = __all_sync(kFull, tc::sleep(raw_full + buf, raw_phase));
-      if (ok) put_chunk<MODE, A, kStride>(sc, u, lane, raw + buf * kRawBytes, m.sf + 512 * group);
-      __syncwarp();
-      if (lane == 0) tc::arrive(m.raw_empty + buf);
+  const int pitch = p.K >> 5;
+  auto serve = [&](int buf) {
+    bool ok = __all_sync(kFull, tc::sleep(raw_full + buf, raw_phase));
+    int stages = 0;
+    if (ok) {
+      stages = *reinterpret_cast<volatile int*>(m.head + 4 * buf);
+      if constexpr (PUT)
+        if (stages > 0)
+          put_chunk<MODE, A, kStride>(*reinterpret_cast<volatile int*>(m.head + 4 * buf + 1 + group),
+                                      pitch, lane, raw + buf * kRawBytes, m.sf + 512 * group);
     }
+    __syncwarp();
+    if (lane == 0) tc::arrive(m.raw_empty + buf);
     if (buf == kRawDepth - 1) raw_phase ^= 1;
     asm volatile("bar.sync 1, 128;" ::: "memory");   // the chunk is in its pieces
     // a stage's words are read before the wait for its slot, and the waits
@@ -504,7 +532,7 @@ __device__ __forceinline__ void gemm_scales(const GroupedGemmParams& p, const Ge
           wb[i][k - 1] = *reinterpret_cast<const uint4*>(piece + 512 * k + 16 * lane);
       }
     };
-    read(0);
+    if (stages > 0) read(0);
     for (int s = 0; s < stages; ++s) {
       ok = ok && __all_sync(kFull, tc::spin(m.empty + slot, phase));
       if (ok) {
@@ -534,29 +562,18 @@ __device__ __forceinline__ void gemm_scales(const GroupedGemmParams& p, const Ge
     int gone;
     asm volatile("{ .reg .pred p, r; setp.ne.s32 p, %1, 0; bar.red.or.pred r, 2, 128, p; "
                  "selp.s32 %0, 1, 0, r; }" : "=r"(gone) : "r"((int)!ok) : "memory");
-    return gone == 0;
+    return gone == 0 && stages > 0;
   };
-  int buf = 0;
-  bool ok = true;
-  for (GemmWalk<C> w(p, first, step, tiles); ok && !w.done(); w.next()) {
-    const GemmTile t = w.tile(p, m, rank);
-    int stages = (t.kb * 32 + C::kStageK - 1) / C::kStageK;
-    ScaleSrc src;
-    if constexpr (PUT) src = scale_src<C>(p, m, t, group);
-    for (int u = 0; ok && stages > 0; stages -= kStagesPerChunk, u += kChunk) {
-      ok = serve(src, u, buf, min(stages, kStagesPerChunk));
-      if (++buf == kRawDepth) buf = 0;
-    }
-  }
+  for (int buf = 0; serve(buf);)
+    if (++buf == kRawDepth) buf = 0;
 }
 
 // The scale warp's role, fixed for the launch.
 template <typename C>
 __device__ __forceinline__ void gemm_scales_any(const GroupedGemmParams& p, const GemmSmem& m,
-                                                uint32_t tbase, int tiles, int first, int step,
-                                                int rank, int group) {
+                                                uint32_t tbase, int group) {
 #define MOEACT_SCALES(MODE, A) \
-  gemm_scales<C, true, MODE, A>(p, m, tbase, tiles, first, step, rank, group)
+  gemm_scales<C, true, MODE, A>(p, m, tbase, group)
 #define MOEACT_SCALES_OF(OUTER, TILED, A)                      \
   if constexpr (OUTER) {                                       \
     if (TILED) MOEACT_SCALES(kTiled, A);                       \
@@ -574,7 +591,7 @@ __device__ __forceinline__ void gemm_scales_any(const GroupedGemmParams& p, cons
   } else if (group < C::kGroups) {
     MOEACT_SCALES_OF(C::kBmn, p.b_tiled, false)
   } else {
-    gemm_scales<C, false, kRows16, false>(p, m, tbase, tiles, first, step, rank, 0);
+    gemm_scales<C, false, kRows16, false>(p, m, tbase, 0);
   }
 #undef MOEACT_SCALES_OF
 #undef MOEACT_SCALES
@@ -689,7 +706,7 @@ __device__ void gemm_mma(const GroupedGemmParams& p, const GemmSmem& m, uint32_t
   int slot = 0, n = 0;
   uint32_t phase = 0;
   for (GemmWalk<C> walk(p, first, step, tiles); !walk.done(); walk.next()) {
-    const int kb = walk.tile(p, m, 0).kb;
+    const int kb = C::kWgrad ? walk.tile(p, m, 0).kb : p.K >> 5;
     if (kb == 0) continue;
     const int mmas = (kb * 32 + C::kMmaK - 1) / C::kMmaK;
     // the tile whose columns this one takes: the last but one, or with
@@ -803,8 +820,8 @@ __device__ void gemm_epilogue(const GroupedGemmParams& p, const GemmSmem& m, con
     const int e_row = (int)tile.row0 + 32 * q;   // row of A, or (wgrad) of dW_e
     const int64_t row = (C::kWgrad ? (int64_t)tile.e * p.R : 0) + e_row;
     auto put = [&](auto out32, const uint4* v, int col) {
-      store_piece<C::kWgrad, decltype(out32)::value, C::kEpiTurns>(p, tm_out, stg, turn, v, row, rows, col,
-                                                     tile.e, e_row, lane);
+      store_piece<C::kWgrad, decltype(out32)::value, C::kEpiTurns>(
+          p, tm_out, stg, turn, v, row, rows, col, tile.e, e_row, lane);
     };
     using Bf16 = std::integral_constant<bool, false>;
     using Fp32 = std::integral_constant<bool, true>;
@@ -901,6 +918,7 @@ __global__ void __launch_bounds__(GemmCfg<OP, PAIR>::kThreads, 1)
   m.d_full = m.raw_empty + kRawDepth;
   m.d_empty = m.d_full + 2;
   m.misc = reinterpret_cast<int*>(bars + 64);
+  m.head = m.misc + 4;
   m.scan = m.misc + 16;
   m.ro = reinterpret_cast<int*>(reinterpret_cast<unsigned char*>(bars) + kGemmMisc);
   m.pre = m.ro + p.E + 1;
@@ -970,7 +988,7 @@ __global__ void __launch_bounds__(GemmCfg<OP, PAIR>::kThreads, 1)
       mbar_init(m.empty + i, 1);
     }
     for (int i = 0; i < C::kGroups * kRawDepth; ++i) mbar_init(m.raw_full + i, 32);
-    for (int i = 0; i < kRawDepth; ++i) mbar_init(m.raw_empty + i, C::kGroups);
+    for (int i = 0; i < kRawDepth; ++i) mbar_init(m.raw_empty + i, 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(m.d_full + i, 1);
       mbar_init(m.d_empty + i, 4 * C::kCG);
@@ -989,7 +1007,7 @@ __global__ void __launch_bounds__(GemmCfg<OP, PAIR>::kThreads, 1)
   const uint32_t tbase = *reinterpret_cast<volatile uint32_t*>(m.misc);
 
   if (warp < 4) gemm_epilogue<C>(p, m, &tm_out, tbase, tiles, first, step, rank);
-  else if (warp < 8)  gemm_scales_any<C>(p, m, tbase, tiles, first, step, rank, warp - 4);
+  else if (warp < 8)  gemm_scales_any<C>(p, m, tbase, warp - 4);
   else if (warp == 8) gemm_producer<C>(p, m, &tm_a, &tm_b, tiles, first, step, rank);
   else if (warp == 10) gemm_scale_loader<C>(p, m, &tm_sa, &tm_sb, tiles, first, step, rank);
   else if (C::kWgrad && warp == 11) gemm_clear<C>(p, m, tiles, first, step, rank);
