@@ -600,57 +600,55 @@ __device__ __forceinline__ void gemm_scales_any(const GroupedGemmParams& p, cons
 // ------------------------------------------------------------ code tiles
 // Warp 8.
 template <typename C>
-__device__ void gemm_producer(const GroupedGemmParams& p, const GemmSmem& m, const void* tm_a,
-                              const void* tm_b, int tiles, int first, int step, int rank) {
-  const bool leader = tc::elect_one();
+__device__ __forceinline__ void gemm_copy_codes(const GroupedGemmParams& p, const GemmSmem& m,
+                                                const void* tm_a, const void* tm_b, int tiles,
+                                                int first, int step, int rank) {
+  // wgrad's copies complete on barriers of this SM's: gemm_clear passes them on
+  const uint32_t bar0 = C::kAmn ? smem_addr(m.landed) : tc::leader_addr(m.full);
   int slot = 0;
   uint32_t phase = 1;
   for (GemmWalk<C> walk(p, first, step, tiles); !walk.done(); walk.next()) {
     const GemmTile tile = walk.tile(p, m, rank);
     const int stages = (tile.kb * 32 + C::kStageK - 1) / C::kStageK;
     const int col_b = tile.n0 + (C::kCG == 2 ? 128 * rank : 0);   // this SM's rows of B
+    // the boxes' rows: of the summed index where that is outermost
+    const int ya = C::kAmn ? (int)tile.k0 : (int)tile.row0;
+    const int yb = C::kAmn ? (int)tile.k0 : C::kBmn ? tile.e * p.K : tile.e * p.N + col_b;
+    const int rows_a = (tile.rows + C::kABox - 1) / C::kABox;
     for (int s = 0; s < stages; ++s) {
-      if (!__all_sync(kFull, tc::spin(m.empty + slot, phase))) {
-        if (leader) gemm_abort(p, m);
+      if (!tc::spin(m.empty + slot, phase)) {
+        gemm_abort(p, m);
         return;
       }
       unsigned char* da = m.stages + slot * C::kStageBytes;
       unsigned char* db = da + kTileBytes;
-      // wgrad's copies complete on a barrier of this SM's: gemm_clear passes
-      // them on
-      const uint32_t bar = C::kAmn ? smem_addr(m.landed + slot) : tc::leader_addr(m.full + slot);
-      int na = 0, nb = 1;   // boxes of A and B
-      if constexpr (C::kAmn) {
-        na = nb = min(4, tile.kb - 4 * s);
-      } else {
-        na = (tile.rows + C::kABox - 1) / C::kABox;
-        if constexpr (C::kBmn) nb = min(4, tile.kb - 4 * s);
-      }
-      if (leader) {
-        const uint32_t bytes = (uint32_t)(na * C::kABox + nb * C::kBBox) * 128u;
-        if constexpr (C::kAmn) mbar_expect_tx(m.landed + slot, bytes);
-        else tc::arrive_tx_cluster(bar, bytes);
-        for (int i = 0; i < na; ++i) {
-          if constexpr (C::kAmn)
-            tc::load_2d<1>(da + i * 4096, tm_a, (int)tile.row0, (int)tile.k0 + 128 * s + 32 * i,
-                           bar);
-          else
-            tc::load_2d<C::kCG>(da + i * C::kABox * 128, tm_a, 128 * s,
-                                (int)tile.row0 + C::kABox * i, bar);
-        }
-        for (int i = 0; i < nb; ++i) {
-          if constexpr (C::kAmn)
-            tc::load_2d<1>(db + i * 4096, tm_b, col_b, (int)tile.k0 + 128 * s + 32 * i, bar);
-          else if constexpr (C::kBmn)
-            tc::load_2d<C::kCG>(db + i * 4096, tm_b, col_b, tile.e * p.K + 128 * s + 32 * i, bar);
-          else
-            tc::load_2d<C::kCG>(db, tm_b, 128 * s, tile.e * p.N + col_b, bar);
-        }
-      }
-      __syncwarp();
+      const uint32_t bar = bar0 + 8 * slot;
+      const int blocks = min(4, tile.kb - 4 * s);
+      const int na = C::kAmn ? blocks : rows_a, nb = C::kBmn ? blocks : 1;
+      const uint32_t bytes = (uint32_t)(na * C::kABox + nb * C::kBBox) * 128u;
+      if constexpr (C::kAmn || C::kCG == 1)
+        tc::arrive_tx(bar, bytes);
+      else
+        tc::arrive_tx_cluster(bar, bytes);
+      constexpr int kLoad = C::kAmn ? 1 : C::kCG;
+      for (int i = 0; i < na; ++i)
+        tc::load_2d<kLoad>(da + i * C::kABox * 128, tm_a, C::kAmn ? (int)tile.row0 : 128 * s,
+                           ya + (C::kAmn ? 128 * s : 0) + C::kABox * i, bar);
+      for (int i = 0; i < nb; ++i)
+        tc::load_2d<kLoad>(db + i * C::kBBox * 128, tm_b, C::kBmn ? col_b : 128 * s,
+                           yb + (C::kBmn ? 128 * s : 0) + C::kBBox * i, bar);
       if (++slot == C::kStages) slot = 0, phase ^= 1;
     }
   }
+}
+
+// (One thread runs the loop: warp-wide votes and barriers in every stage cost 1 to
+// 7% of products over short sums.)
+template <typename C>
+__device__ void gemm_producer(const GroupedGemmParams& p, const GemmSmem& m, const void* tm_a,
+                              const void* tm_b, int tiles, int first, int step, int rank) {
+  if (tc::elect_one()) gemm_copy_codes<C>(p, m, tm_a, tm_b, tiles, first, step, rank);
+  __syncwarp();
 }
 
 // Warp 11, wgrad: once a stage has landed, clears the rows past the group's end

@@ -342,6 +342,76 @@ def test_graph_replay_with_new_rows(cuda_device):
         _check(dw, dwant, dsize, 201, "wgrad")
 
 
+def test_offsets_past_32_bits(cuda_device):
+    """Outputs and gradients of more than 2^31 values: the last rows land where
+    they belong."""
+    g = _gen(14)
+    M, K, N = 66049, 32, 33024
+    a, sa, w, sw = _codes(g, M, K), _scales(g, M, 1), _codes(g, N, K), _scales(g, N, 1)
+    out, _ = mg.grouped_mxfp8_gemm(mg.MXFP8(a, None, sa, None), mg.MXFP8(w, None, sw, None),
+                                   _dev([0, M]))
+    assert out.numel() > 2 ** 31
+    av, wv = ref.values8(a[-300:], sa[-300:], 1), ref.values8(w, sw, 1)
+    _check(out[-300:], av @ wv.T, av.abs() @ wv.abs().T, K, "gemm")
+    del out, wv
+    E, H, K = 3, 32768, 32768
+    dy, x = _codes(g, 40, H), _codes(g, 40, K)
+    sy, sx = _scales(g, 3, H), _scales(g, 3, K)
+    ro, cb = _dev([0, 0, 7, 40]), _dev([0, 0, 1, 3])
+    dw, _ = mg.grouped_mxfp8_wgrad(mg.MXFP8(None, dy, None, sy), mg.MXFP8(None, x, None, sx), ro, cb,
+                                   out_dtype=torch.bfloat16)
+    yv, xv = ref.values8(dy, sy, 0, [0, 0, 7, 40])[7:], ref.values8(x, sx, 0, [0, 0, 7, 40])[7:]
+    h = yv[:, -130:]
+    _check(dw[2, -130:], h.T @ xv, h.abs().T @ xv.abs(), 33, "wgrad")
+    assert bool((dw[0] == 0).all())
+
+
+def test_most_groups(cuda_device):
+    """MAX_GROUPS groups, most of them empty, on one SM and on pairs."""
+    E, K, H = _capi.MAX_GROUPS, 64, 32
+    splits = [3 if e % 50 == 7 else 0 for e in range(E)]
+    for op in ("gemm", "dgrad", "gemm4"):
+        call, want, size, n, _, _ = _rows_case(op, splits, K, H, 15)
+        out, st = call()
+        assert int(st) == 0
+        _check(out, want, size, n, op)
+    splits[11] = 300000
+    call, want, size, n, _, _ = _rows_case("gemm", splits, K, H, 16)
+    out, st = call()
+    assert int(st) == 0
+    _check(out, want, size, n, "many rows")
+    dy, x, sy, sx, ro, cb, want, size = _wgrad_case([e % 3 for e in range(E)], 160, 64, 17)
+    dw, st = mg.grouped_mxfp8_wgrad(mg.MXFP8(None, dy, None, sy), mg.MXFP8(None, x, None, sx), ro, cb)
+    assert int(st) == 0
+    _check(dw, want, size, 2, "wgrad")
+
+
+@pytest.mark.parametrize("pitch_k", [32 * k for k in (1, 2, 3, 4, 7, 8, 12, 15, 16, 20, 24, 31, 32,
+                                                      33, 36, 40, 48, 64, 65, 66, 68, 80)])
+def test_scale_row_lengths(cuda_device, pitch_k):
+    """Every way the rows' scales are copied (rows of 1 to 80 bytes, groups at odd
+    rows), single SMs and pairs."""
+    for splits, H in (([5, 0, 1, 130, 40], 96), ([1031, 0, 900], 1376)):
+        for op in ("gemm", "gemm4"):
+            call, want, size, n, _, _ = _rows_case(op, splits, pitch_k, H, pitch_k)
+            out, _ = call(out_dtype=torch.float32)
+            _check(out, want, size, n, (op, splits, pitch_k))
+
+
+def test_scales_and_codes_at_the_end_of_their_memory(cuda_device):
+    """Rows in the middle of larger buffers, their neighbours NaN: nothing beyond
+    the rows' own bytes takes part."""
+    M, K, H = 37, 96, 64
+    call, want, size, n, _, (a, sa, w, sw, ro) = _rows_case("gemm4", [20, 17], K, H, 18)
+    def inside(t):
+        flat = torch.full((t.numel() + 512,), 255, dtype=torch.uint8, device="cuda")
+        v = flat[256:256 + t.numel()].view(t.shape)
+        v.copy_(t)
+        return v
+    out, _ = mg.grouped_mxfp4_gemm(mg.MXFP4(inside(a), inside(sa)), mg.MXFP4(inside(w), inside(sw)), ro)
+    _check(out, want, size, n, "inside")
+
+
 def test_results_repeat(cuda_device):
     """The same call gives the same bits."""
     call, *_ = _rows_case("dgrad", [700, 0, 1300, 130], 1056, 2592, 11)
