@@ -521,8 +521,9 @@ def grouped_scaled_swiglu_mxfp8_fc2(x, s, row_offs, w_codes, w_scales, *, status
 
 
 # ------------------------------------------------------------------ plain quantizers
-# (These calls are short next to a small product's few microseconds, so their
-# checks read each tensor attribute once.)
+# (A small quantizer or product takes a few microseconds on the GPU, so these
+# calls read each tensor attribute once and pass sizes as plain arguments: 0.7 us
+# less per torch.empty than a tuple.)
 _U8, _F8, _BF16, _F32 = torch.uint8, torch.float8_e4m3fn, torch.bfloat16, torch.float32
 
 
@@ -530,7 +531,7 @@ def _call_on(dev, name, *args):
     """Calls the library with `dev` current (the tensors' device may be another
     than the current one), on that device's current stream."""
     index = dev.index
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         st = getattr(_capi.lib(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(dev):
@@ -601,11 +602,11 @@ def _quantize8(x, rowwise, colwise, gemm_scales, noop_flag, out, grouped):
     rq = rs = cq = cs = None
     if out is None:
         if rowwise:
-            rq = torch.empty((M, N), dtype=_F8, device=dev)
-            rs = torch.empty((M, N // 32), dtype=_U8, device=dev)
+            rq = torch.empty(M, N, dtype=_F8, device=dev)
+            rs = torch.empty(M, N // 32, dtype=_U8, device=dev)
         if colwise:
-            cq = torch.empty((M, N), dtype=_F8, device=dev)
-            cs = torch.empty((col_rows, N), dtype=_U8, device=dev)
+            cq = torch.empty(M, N, dtype=_F8, device=dev)
+            cs = torch.empty(col_rows, N, dtype=_U8, device=dev)
     else:
         rq, rs, cq, cs = _take_mx(out, M, N, dirs, dev, col_rows)
         rq, cq = rq.view(_F8), cq.view(_F8)
@@ -671,8 +672,8 @@ def mxfp4_quantize(x, *, gemm_scales=False, noop_flag=None, out=None):
     if N % 32 or N == 0:
         raise ValueError(f"x must have a positive multiple of 32 columns, got {N}")
     if out is None:
-        out = MXFP4(torch.empty((M, N // 2), dtype=_U8, device=dev),
-                    torch.empty((M, N // 32), dtype=_U8, device=dev))
+        out = MXFP4(torch.empty(M, N // 2, dtype=_U8, device=dev),
+                    torch.empty(M, N // 32, dtype=_U8, device=dev))
         codes, scales = out.codes.data_ptr(), out.scales.data_ptr()
     else:
         codes = _u8(out.codes, "out.codes", (M, N // 2), dev)
@@ -694,7 +695,7 @@ def mxfp4_dequantize(q, *, gemm_scales=False, noop_flag=None, out=None):
     codes = _u8(q.codes, "codes", (M, N // 2), dev)
     scales = _u8(q.scales, "scales", (M, N // 32), dev)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        out = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
     elif out.dtype != _BF16 or out.shape != (M, N) or out.stride(1) != 1 or out.device != dev:
         raise ValueError(f"out must be a bf16 [{M}, {N}] tensor with unit column stride on {dev}")
     flag = _flag(noop_flag, dev)
@@ -747,7 +748,7 @@ def _product(name, codes, scales, per_byte, w_codes, w_scales, w_inner, row_offs
     sw = _u8(w_scales, "w scales", (rows, K // 32) if w_inner else (rows // 32, width), dev)
     dt, code = _out_dtype(out_dtype, out)
     if out is None:
-        out = torch.empty((M, N), dtype=dt, device=dev)
+        out = torch.empty(M, N, dtype=dt, device=dev)
         stride = N
     else:
         if out.shape != (M, N) or out.stride(1) != 1 or out.device != dev:
@@ -823,7 +824,7 @@ def grouped_mxfp8_wgrad(dy, x, row_offs, colblk_offs, *, out_dtype=torch.float32
     if accumulate and dt != _F32:
         raise TypeError("accumulate needs a float32 out")
     if out is None:
-        out = torch.empty((E, H, K), dtype=dt, device=dev)
+        out = torch.empty(E, H, K, dtype=dt, device=dev)
     elif out.shape != (E, H, K) or not out.is_contiguous() or out.device != dev:
         raise ValueError(f"out must be a contiguous [{E}, {H}, {K}] tensor on {dev}")
     status = _status(status, dev)
