@@ -1,7 +1,8 @@
 /*
  * moeact.h -- C ABI of libmoeact.so: per-row-scaled gated activation
  * (SwiGLU, SReLU) fused with MXFP8 quantization, forward and backward, dense
- * and grouped (MoE experts), for NVIDIA B200 (sm_100a).
+ * and grouped (MoE experts), plain MXFP8 / MXFP4 quantizers and the grouped
+ * products of their outputs, for NVIDIA B200 (sm_100a).
  *
  * What the calls compute is defined by these pages (title, section):
  *   [AO]   pytorch/ao PR #4743 "[mxfp8 training] Add a fused gated-activation

@@ -13,10 +13,10 @@
 //              memory -> bulk tensor stores of 32 rows x 128 bytes;
 //   warps 4-7  scales: E8M0 words from shared memory, as they came, into the
 //              order of tensor memory and each stage's there (tcgen05.st);
-//   warp 10    the scales' copies into shared memory, some chunks ahead;
-//   warp 11    wgrad: clears the rows past a group's end;
 //   warp 8     TMA loads of the code tiles (128 rows x 128 bytes each);
-//   warp 9     tensor-memory allocation; in the pair's first SM the MMAs.
+//   warp 9     tensor-memory allocation; in the pair's first SM the MMAs;
+//   warp 10    the scales' copies into shared memory, some chunks ahead;
+//   warp 11    wgrad: clears the rows past a group's end.
 // One ring of stages carries codes and scales: `full` collects the TMA bytes
 // and the scale warps of both SMs, `empty` comes from the MMAs' commit.
 //
@@ -29,6 +29,7 @@
 // lets what is in flight finish (bounded) and returns.
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "grouped_gemm.cuh"
@@ -45,6 +46,11 @@ constexpr int kChunk = 8;                 // scale words of a row fetched togeth
 constexpr int kRawDepth = 2;              // chunks on their way
 constexpr int kRawBytes = 128 * 36;       // a chunk of 128 rows as it arrives
 
+// The groups' tables: two words a group, one (`pre`) above kGroupsInSmem groups,
+// whose row offsets are read from global memory.
+constexpr int kGroupsInSmem = 1200;
+constexpr int group_bytes_gemm(int E) { return (E + 1) * (E <= kGroupsInSmem ? 8 : 4); }
+
 template <int OP, bool PAIR>
 struct GemmCfg {
   static constexpr bool kF4 = OP == kGemmFwd4;
@@ -55,7 +61,9 @@ struct GemmCfg {
   static constexpr int kCG = PAIR ? 2 : 1;
   static constexpr int kTM = 128 * kCG;
   static constexpr int kBN = PAIR ? 256 : 128;
-  static constexpr int kStages = PAIR ? 4 : 5;
+  // wgrad's short sums leave its epilogue the bottleneck: it has the second
+  // staging buffer, the others the fifth stage
+  static constexpr int kStages = PAIR && kWgrad ? 4 : 5;
   static constexpr int kStageK = kF4 ? 256 : 128;      // summed index per stage
   static constexpr int kMmaK = kF4 ? 64 : 32;
   static constexpr int kWords = kF4 ? 2 : 1;           // scale words per row and stage
@@ -70,11 +78,13 @@ struct GemmCfg {
   static constexpr int kGroups = 1 + kBN / 128;        // 128-row groups of scales (and warps)
   static constexpr int kSfBytes = kChunk * kGroups * 512;   // a chunk, ready for tensor memory
   static constexpr int kRawGroupBytes = kRawDepth * kRawBytes;
-  static constexpr int kEpiTurns = PAIR ? 2 : 1;       // staging buffers of an epilogue warp
+  static constexpr int kEpiTurns = PAIR && kWgrad ? 2 : 1;   // staging buffers of an epilogue warp
   static constexpr int kEpiWarpBytes = kEpiTurns * kPieceBytes;
   static constexpr int kFixed = kStages * kStageBytes + 4 * kEpiWarpBytes + kSfBytes +
                                 kGroups * kRawGroupBytes + kGemmMisc;
-  static_assert(kFixed + 1024 + 8 * 2041 <= 232448, "shared memory of a block");
+  static_assert(kFixed + 1024 + group_bytes_gemm(2040) <= 232448 &&
+                    kFixed + 1024 + group_bytes_gemm(kGroupsInSmem) <= 232448,
+                "shared memory of a block");
   static_assert(kAcc1 >= 0 && kAcc1 + kBN <= kSfCol, "tensor-memory columns overlap");
   static_assert(kOverlap % 64 == 0, "the overlap is drained in chunks of 64 columns");
 };
@@ -94,7 +104,7 @@ struct GemmSmem {
   int* head;           // [kRawDepth][4] of a raw chunk: its stages, the groups' places (ScaleHead)
   int* misc;           // [0] tensor-memory base, [1] abort
   int* scan;           // [12] warp totals
-  int* ro;             // [E + 1] the row offsets (below 2^30)
+  int* ro;             // [E + 1] the row offsets (below 2^30); null: too many
   int* pre;            // [E + 1] row tiles before each expert; wgrad: scale rows before it
 };
 
@@ -137,6 +147,9 @@ struct GemmWalk {
     dn = step - dm * nt;
   }
   __device__ __forceinline__ bool done() const { return t >= tiles; }
+  __device__ __forceinline__ int row_off(const GroupedGemmParams& p, const GemmSmem& m, int g) {
+    return m.ro != nullptr ? m.ro[g] : (int)p.row_offs[g];
+  }
   __device__ __forceinline__ void next() {
     t += step;
     mt += dm;
@@ -152,8 +165,8 @@ struct GemmWalk {
       e = mt / ht;
       r.row0 = (mt - e * ht) * C::kTM + 128 * rank;
       r.rows = max(0, min(128, p.R - (int)r.row0));
-      r.k0 = m.ro[e];
-      r.krows = m.ro[e + 1] - (int)r.k0;
+      r.k0 = row_off(p, m, e);
+      r.krows = row_off(p, m, e + 1) - (int)r.k0;
       r.kb = (r.krows + 31) >> 5;
     } else {
       int hi = p.E - 1;   // largest e with pre[e] <= mt (then mt < pre[e + 1])
@@ -161,8 +174,8 @@ struct GemmWalk {
         const int mid = (e + hi + 1) >> 1;
         if (m.pre[mid] <= mt) e = mid; else hi = mid - 1;
       }
-      r.row0 = m.ro[e] + (mt - m.pre[e]) * C::kTM + 128 * rank;
-      r.rows = max(0, min(128, m.ro[e + 1] - (int)r.row0));
+      r.row0 = row_off(p, m, e) + (mt - m.pre[e]) * C::kTM + 128 * rank;
+      r.rows = max(0, min(128, row_off(p, m, e + 1) - (int)r.row0));
       r.k0 = 0;
       r.krows = 0;
       r.kb = p.K >> 5;
@@ -448,7 +461,10 @@ __device__ void gemm_scale_loader(const GroupedGemmParams& p, const GemmSmem& m,
 #pragma unroll 1
       for (int g = 0; g < C::kGroups; ++g) {
         const ScaleSrc src = scale_src<C>(p, m, t, g);
-        if (lane == 0) m.head[4 * buf + 1 + g] = scale_head<C>(src, u);
+        if (lane == 0) {
+          m.head[4 * buf + 1 + g] = scale_head<C>(src, u);
+          __threadfence_block();   // (an arrival by cp.async does not order it)
+        }
         unsigned char* raw = m.raw + g * C::kRawGroupBytes + buf * kRawBytes;
         uint64_t* bar = m.raw_full + g * kRawDepth + buf;
         const int mode = g == 0 ? mode_a : mode_b;
@@ -918,8 +934,8 @@ __global__ void __launch_bounds__(GemmCfg<OP, PAIR>::kThreads, 1)
   m.misc = reinterpret_cast<int*>(bars + 64);
   m.head = m.misc + 4;
   m.scan = m.misc + 16;
-  m.ro = reinterpret_cast<int*>(reinterpret_cast<unsigned char*>(bars) + kGemmMisc);
-  m.pre = m.ro + p.E + 1;
+  m.pre = reinterpret_cast<int*>(reinterpret_cast<unsigned char*>(bars) + kGemmMisc);
+  m.ro = p.E <= kGroupsInSmem ? m.pre + p.E + 1 : nullptr;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     tc::prefetch_map(&tm_a);
@@ -937,8 +953,10 @@ __global__ void __launch_bounds__(GemmCfg<OP, PAIR>::kThreads, 1)
   int local = 0, bad = 0;
   for (int e = e_lo; e < e_hi; ++e) {
     const int64_t r0 = p.row_offs[e], r1 = p.row_offs[e + 1];
-    m.ro[e] = (int)r0;
-    m.ro[e + 1] = (int)r1;   // (the next thread's first writes the same)
+    if (m.ro != nullptr) {
+      m.ro[e] = (int)r0;
+      m.ro[e + 1] = (int)r1;   // (the next thread's first writes the same)
+    }
     if (r1 < r0 || r0 < 0 || r1 > p.M) bad |= 1;
     else local += (int)((r1 - r0 + C::kTM - 1) / C::kTM);
     if constexpr (C::kWgrad) {
@@ -969,7 +987,7 @@ __global__ void __launch_bounds__(GemmCfg<OP, PAIR>::kThreads, 1)
   if constexpr (!C::kWgrad) {
     for (int e = e_lo; e < e_hi; ++e) {
       m.pre[e] = before;
-      before += (m.ro[e + 1] - m.ro[e] + C::kTM - 1) / C::kTM;
+      before += (int)((p.row_offs[e + 1] - p.row_offs[e] + C::kTM - 1) / C::kTM);
     }
     if (tid == 0) m.pre[E] = total;
   } else {
@@ -1031,14 +1049,15 @@ __global__ void __launch_bounds__(GemmCfg<OP, PAIR>::kThreads, 1)
 template <int OP, bool PAIR>
 int gemm_smem_bytes(int E) {
   using C = GemmCfg<OP, PAIR>;
-  return 1024 + C::kFixed + (E + 1) * 8;
+  return 1024 + C::kFixed + group_bytes_gemm(E);
 }
 
 template <int OP, bool PAIR>
 cudaError_t gemm_prepare_one(int max_groups) {
   return cudaFuncSetAttribute(grouped_gemm_kernel<OP, PAIR>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              gemm_smem_bytes<OP, PAIR>(max_groups));
+                              std::max(gemm_smem_bytes<OP, PAIR>(max_groups),
+                                       gemm_smem_bytes<OP, PAIR>(kGroupsInSmem)));
 }
 
 template <int OP, bool PAIR>
