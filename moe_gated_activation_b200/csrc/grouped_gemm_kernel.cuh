@@ -16,7 +16,8 @@
 //   warp 8     TMA loads of the code tiles (128 rows x 128 bytes each);
 //   warp 9     tensor-memory allocation; in the pair's first SM the MMAs;
 //   warp 10    the scales' copies into shared memory, some chunks ahead;
-//   warp 11    wgrad: clears the rows past a group's end.
+//   warp 11    wgrad: clears the rows past a group's end;
+//   warps 12-15  wgrad on pairs: a second set of epilogue warps.
 // One ring of stages carries codes and scales: `full` collects the TMA bytes
 // and the scale warps of both SMs, `empty` comes from the MMAs' commit.
 //
@@ -57,13 +58,15 @@ struct GemmCfg {
   static constexpr bool kWgrad = OP == kGemmWgrad;
   static constexpr bool kAmn = OP == kGemmWgrad;                      // A rows = summed index
   static constexpr bool kBmn = OP == kGemmWgrad || OP == kGemmDgrad;  // B rows = summed index
-  static constexpr int kThreads = kWgrad ? 384 : 352;
+  // wgrad on pairs: short sums, so a second set of epilogue warps (12-15) takes
+  // half of the columns
+  static constexpr int kSets = PAIR && kWgrad ? 2 : 1;
+  static constexpr int kThreads = kSets == 2 ? 512 : kWgrad ? 384 : 352;
   static constexpr int kCG = PAIR ? 2 : 1;
   static constexpr int kTM = 128 * kCG;
   static constexpr int kBN = PAIR ? 256 : 128;
-  // wgrad's short sums leave its epilogue the bottleneck: it has the second
-  // staging buffer, the others the fifth stage
-  static constexpr int kStages = PAIR && kWgrad ? 4 : 5;
+  // (the second set's staging takes the place of a fifth stage)
+  static constexpr int kStages = kSets == 2 ? 4 : 5;
   static constexpr int kStageK = kF4 ? 256 : 128;      // summed index per stage
   static constexpr int kMmaK = kF4 ? 64 : 32;
   static constexpr int kWords = kF4 ? 2 : 1;           // scale words per row and stage
@@ -78,9 +81,7 @@ struct GemmCfg {
   static constexpr int kGroups = 1 + kBN / 128;        // 128-row groups of scales (and warps)
   static constexpr int kSfBytes = kChunk * kGroups * 512;   // a chunk, ready for tensor memory
   static constexpr int kRawGroupBytes = kRawDepth * kRawBytes;
-  static constexpr int kEpiTurns = PAIR && kWgrad ? 2 : 1;   // staging buffers of an epilogue warp
-  static constexpr int kEpiWarpBytes = kEpiTurns * kPieceBytes;
-  static constexpr int kFixed = kStages * kStageBytes + 4 * kEpiWarpBytes + kSfBytes +
+  static constexpr int kFixed = kStages * kStageBytes + 4 * kSets * kPieceBytes + kSfBytes +
                                 kGroups * kRawGroupBytes + kGemmMisc;
   static_assert(kFixed + 1024 + group_bytes_gemm(2040) <= 232448 &&
                     kFixed + 1024 + group_bytes_gemm(kGroupsInSmem) <= 232448,
@@ -103,7 +104,7 @@ struct GemmSmem {
   uint64_t* d_empty;   // [2] (first SM) its columns may be overwritten
   int* head;           // [kRawDepth][4] of a raw chunk: its stages, the groups' places (ScaleHead)
   int* misc;           // [0] tensor-memory base, [1] abort
-  int* scan;           // [12] warp totals
+  int* scan;           // [16] warp totals
   int* ro;             // [E + 1] the row offsets (below 2^30); null: too many
   int* pre;            // [E + 1] row tiles before each expert; wgrad: scale rows before it
 };
@@ -767,28 +768,26 @@ __device__ void gemm_mma(const GroupedGemmParams& p, const GemmSmem& m, uint32_t
 // 32 rows x 128 bytes from registers (thread t: row t, as eight 16-byte
 // pieces) into the warp's staging, swizzled (piece c of row r at c ^ (r mod
 // 8)), and from there to the output: whole pieces by one bulk tensor store,
-// which clips columns past the output's and leaves the warp free (the TURNS
-// staging buffers take turns); pieces with fewer rows, and sums with what the output
-// holds, by plain stores of whole row segments.
-template <bool WGRAD, bool OUT32, int TURNS>
+// which clips columns past the output's and leaves the warp free; pieces with
+// fewer rows, and sums with what the output holds, by plain stores of whole
+// row segments.
+template <bool WGRAD, bool OUT32>
 __device__ __forceinline__ void store_piece(const GroupedGemmParams& p, const void* tm_out,
-                                            unsigned char* stg, int& turn, const uint4* v,
+                                            unsigned char* stg, const uint4* v,
                                             int64_t row, int rows, int col, int e, int e_row,
                                             int lane) {
   constexpr int kPer = OUT32 ? 4 : 8;   // columns in 16 bytes
-  unsigned char* buf = stg + turn * kPieceBytes;
-  if (TURNS > 1) turn ^= 1;
-  if (lane == 0) tc::bulk_wait_read<TURNS - 1>();   // this buffer's last store has read it
+  if (lane == 0) tc::bulk_wait_read();   // the last store has read the staging
   __syncwarp();
 #pragma unroll
   for (int c = 0; c < 8; ++c)
-    *reinterpret_cast<uint4*>(buf + lane * 128 + ((c ^ (lane & 7)) << 4)) = v[c];
+    *reinterpret_cast<uint4*>(stg + lane * 128 + ((c ^ (lane & 7)) << 4)) = v[c];
   if ((WGRAD || rows == 32) && !p.accumulate) {
     tc::fence_proxy_async();
     __syncwarp();
     if (lane == 0) {
-      if constexpr (WGRAD) tc::store_3d(tm_out, buf, col, e_row, e);
-      else tc::store_2d(tm_out, buf, col, (int)row);
+      if constexpr (WGRAD) tc::store_3d(tm_out, stg, col, e_row, e);
+      else tc::store_2d(tm_out, stg, col, (int)row);
       tc::bulk_commit();
     }
     __syncwarp();
@@ -800,7 +799,7 @@ __device__ __forceinline__ void store_piece(const GroupedGemmParams& p, const vo
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const int r = 4 * k + (lane >> 3);
-    uint4 w = *reinterpret_cast<const uint4*>(buf + r * 128 + ((c ^ (r & 7)) << 4));
+    uint4 w = *reinterpret_cast<const uint4*>(stg + r * 128 + ((c ^ (r & 7)) << 4));
     if (in && r < rows) {
       if constexpr (OUT32) {
         float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + (row + r) * p.ldo +
@@ -824,18 +823,21 @@ __device__ __forceinline__ void store_piece(const GroupedGemmParams& p, const vo
 
 template <typename C>
 __device__ void gemm_epilogue(const GroupedGemmParams& p, const GemmSmem& m, const void* tm_out,
-                              uint32_t tbase, int tiles, int first, int step, int rank) {
+                              uint32_t tbase, int tiles, int first, int step, int rank,
+                              int set) {
   const int q = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
-  unsigned char* stg = m.epi + q * C::kEpiWarpBytes;
-  int n = 0, turn = 0;
+  unsigned char* stg = m.epi + (4 * set + q) * kPieceBytes;
+  constexpr int kChunks = C::kBN / 64 / C::kSets;   // of 64 columns, of this set
+  const uint32_t d_empty = tc::leader_addr(m.d_empty);
+  int n = 0;
   for (GemmWalk<C> walk(p, first, step, tiles); !walk.done(); walk.next()) {
     const GemmTile tile = walk.tile(p, m, rank);
     const int rows = max(0, min(32, tile.rows - 32 * q));
     const int e_row = (int)tile.row0 + 32 * q;   // row of A, or (wgrad) of dW_e
     const int64_t row = (C::kWgrad ? (int64_t)tile.e * p.R : 0) + e_row;
     auto put = [&](auto out32, const uint4* v, int col) {
-      store_piece<C::kWgrad, decltype(out32)::value, C::kEpiTurns>(
-          p, tm_out, stg, turn, v, row, rows, col, tile.e, e_row, lane);
+      store_piece<C::kWgrad, decltype(out32)::value>(p, tm_out, stg, v, row, rows, col, tile.e,
+                                                     e_row, lane);
     };
     using Bf16 = std::integral_constant<bool, false>;
     using Fp32 = std::integral_constant<bool, true>;
@@ -845,7 +847,8 @@ __device__ void gemm_epilogue(const GroupedGemmParams& p, const GemmSmem& m, con
 #pragma unroll
       for (int i = 0; i < 8; ++i) z[i] = make_uint4(0u, 0u, 0u, 0u);
       const int per = p.out32 ? 32 : 64;
-      for (int c = tile.n0; c < min(tile.n0 + C::kBN, p.N); c += per) {
+      const int c0 = tile.n0 + 64 * kChunks * set;
+      for (int c = c0; c < min(c0 + 64 * kChunks, p.N); c += per) {
         if (p.out32) put(Fp32(), z, c);
         else put(Bf16(), z, c);
       }
@@ -858,23 +861,30 @@ __device__ void gemm_epilogue(const GroupedGemmParams& p, const GemmSmem& m, con
     }
     tc::fence_after();
     const uint32_t src = tbase + ((uint32_t)(32 * q) << 16) + (uint32_t)(b * C::kAcc1);
-    constexpr int kChunks = C::kBN / 64, kOver = C::kOverlap / 64;
+    // The overlapping columns first: the first accumulator's last chunks, the
+    // second one's first.  The columns may be overwritten by the tile after the
+    // next once they are read here, and by the next one's where they overlap: a
+    // set without overlapping columns only says that it is through with the
+    // tile before this one.
+    constexpr int kOver = C::kOverlap / 64;
+    const bool over = C::kSets == 1 || (b == 0) == (set == 1);
+    auto release = [&]() {
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::arrive_cluster(d_empty + 8 * b);
+    };
+    if (!over) release();
 #pragma unroll 1
     for (int i = 0; i < kChunks; ++i) {
-      // the overlapping columns first: the first accumulator's last chunks,
-      // the second one's first
-      const int c = kOver && b == 0 ? (i + kChunks - kOver) % kChunks : i;
+      const int c = kChunks * set +
+                    (kOver && b == 0 && over ? (i + kChunks - kOver) % kChunks : i);
       uint32_t v[64];
       tc::ld32(src + 64 * c, v);
       tc::ld32(src + 64 * c + 32, v + 32);
       tc::wait_ld();
       tc::tie(v);
       tc::tie(v + 32);
-      if (i == (kOver ? kOver : kChunks) - 1) {
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) tc::arrive_cluster(tc::leader_addr(m.d_empty + b));
-      }
+      if (over && i == (kOver ? kOver : kChunks) - 1) release();
       const int col = tile.n0 + 64 * c;
       if (col >= p.N || rows == 0) continue;
       if (p.out32) {
@@ -921,7 +931,7 @@ __global__ void __launch_bounds__(GemmCfg<OP, PAIR>::kThreads, 1)
   GemmSmem m;
   m.stages = base;
   m.epi = base + C::kStages * C::kStageBytes;
-  m.sf = m.epi + 4 * C::kEpiWarpBytes;
+  m.sf = m.epi + 4 * C::kSets * kPieceBytes;
   m.raw = m.sf + C::kSfBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(m.raw + C::kGroups * C::kRawGroupBytes);
   m.full = bars;
@@ -1007,7 +1017,7 @@ __global__ void __launch_bounds__(GemmCfg<OP, PAIR>::kThreads, 1)
     for (int i = 0; i < kRawDepth; ++i) mbar_init(m.raw_empty + i, 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(m.d_full + i, 1);
-      mbar_init(m.d_empty + i, 4 * C::kCG);
+      mbar_init(m.d_empty + i, 4 * C::kSets * C::kCG);
     }
     m.misc[1] = 0;
     mbar_init_fence();
@@ -1022,7 +1032,8 @@ __global__ void __launch_bounds__(GemmCfg<OP, PAIR>::kThreads, 1)
   tc::fence_after();
   const uint32_t tbase = *reinterpret_cast<volatile uint32_t*>(m.misc);
 
-  if (warp < 4) gemm_epilogue<C>(p, m, &tm_out, tbase, tiles, first, step, rank);
+  if (warp < 4 || warp >= 12)
+    gemm_epilogue<C>(p, m, &tm_out, tbase, tiles, first, step, rank, warp >= 12);
   else if (warp < 8)  gemm_scales_any<C>(p, m, tbase, warp - 4);
   else if (warp == 8) gemm_producer<C>(p, m, &tm_a, &tm_b, tiles, first, step, rank);
   else if (warp == 10) gemm_scale_loader<C>(p, m, &tm_sa, &tm_sb, tiles, first, step, rank);
