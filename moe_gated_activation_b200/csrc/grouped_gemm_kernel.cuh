@@ -280,7 +280,8 @@ __device__ __forceinline__ void start_chunk(const ScaleSrc& c, const void* tmap,
   if constexpr (MODE == kCols || MODE == kRows16) {
     if (lane == 0) {
       // 32 block rows of 128 columns, or 32 bytes of up to 128 rows
-      const int boxes = n == 0 ? 0 : MODE == kCols ? 1 : box_rows == 128 ? 1 : (min(128, c.n) + 31) / 32;
+      const int boxes = n == 0 ? 0
+                        : MODE == kCols || box_rows == 128 ? 1 : (min(128, c.n) + 31) / 32;
       mbar_expect_tx(bar, boxes * (MODE == kCols ? 4096 : 32 * box_rows));
       for (int i = 0; i < boxes; ++i)
         tc::load_2d<1>(raw + 1024 * i, tmap, MODE == kCols ? c.c0 : 4 * u,
@@ -1034,11 +1035,11 @@ __global__ void __launch_bounds__(GemmCfg<OP, PAIR>::kThreads, 1)
 
   if (warp < 4 || warp >= 12)
     gemm_epilogue<C>(p, m, &tm_out, tbase, tiles, first, step, rank, warp >= 12);
-  else if (warp < 8)  gemm_scales_any<C>(p, m, tbase, warp - 4);
+  else if (warp < 8) gemm_scales_any<C>(p, m, tbase, warp - 4);
   else if (warp == 8) gemm_producer<C>(p, m, &tm_a, &tm_b, tiles, first, step, rank);
   else if (warp == 10) gemm_scale_loader<C>(p, m, &tm_sa, &tm_sb, tiles, first, step, rank);
   else if (C::kWgrad && warp == 11) gemm_clear<C>(p, m, tiles, first, step, rank);
-  else if (rank == 0) gemm_mma<C>(p, m, tbase, tiles, first, step);
+  else if (warp == 9 && rank == 0) gemm_mma<C>(p, m, tbase, tiles, first, step);
 
   tc::fence_before();
   __syncthreads();
