@@ -483,8 +483,9 @@ moeact_status mxfp4_dequantize(const void* codes, const void* scales, int32_t sc
  *   grouped_mxfp8_wgrad  dW_e[h, k] = sum_i dY[i, h] X[i, k]  (i over group e)
  * for row i of group e, of the values the codes and scales stand for.
  * Products are summed in fp32 by the tensor cores (order not specified); the
- * sum is rounded once to the output type.  A NaN scale or code makes the
- * outputs it enters NaN.
+ * sum is rounded once to the output type.  For fp32 outputs sums of more than
+ * 256 steps (of 32 products, MXFP4 64) are made in parts, which are added in
+ * fp32.  A NaN scale or code makes the outputs it enters NaN.
  *   A, dY (gemm, dgrad)  rowwise codes [M, K] (dgrad [M, H]; MXFP4: [M, K/2]
  *             bytes) and scales [M, K/32] ([M, H/32]) in their scale layout.
  *   W (gemm)  rowwise codes and scales of the dense [E * H, K] matrix.
@@ -503,7 +504,8 @@ moeact_status mxfp4_dequantize(const void* codes, const void* scales, int32_t sc
  *   out       bf16 or fp32 (out_dtype), rows at a stride of ldo >= the width,
  *             a multiple of 16 bytes; columns past the width are not touched.
  *             wgrad: dw [E, H, K] contiguous; groups without rows get zeros;
- *             accumulate = 1 (fp32 only) adds to what dw holds.
+ *             accumulate = 1 (fp32 only) adds to what dw holds (rounded to
+ *             nearest; the memory's adders take subnormals as zero).
  *   status    int32 (device): MOEACT_DEV_OK, or MOEACT_DEV_BAD_OFFSETS /
  *             MOEACT_DEV_UNALIGNED_GROUPS, in which case nothing is written.
  * Every pointer 16-byte aligned (offsets 8, status and noop_flag 4), else

@@ -52,6 +52,16 @@ constexpr int kRawBytes = 128 * 36;       // a chunk of 128 rows as it arrives
 constexpr int kGroupsInSmem = 1200;
 constexpr int group_bytes_gemm(int E) { return (E + 1) * (E <= kGroupsInSmem ? 8 : 4); }
 
+// The tensor cores drop what falls below an accumulator's last bit instead of
+// rounding it: one sum over 65,536 rows of 2^23 and then 2^-5 a step lost every
+// later step, 64 in all, and wgrad of random codes was off by 1.1e-10 times the
+// rows relative to the norm (6.8e-6 at 62,348).  fp32 outputs therefore take a
+// sum in segments of this many steps, which the epilogue adds with rounding
+// (at most 6.7e-7 there; shorter sums keep their time, one group of 65,536
+// rows, 2048 x 1536, takes 230 us for 215).  bf16 ones, whose own rounding is
+// 2^-8, take one sum.  A multiple of a stage's 4 steps.
+constexpr int kSegment = 256;
+
 template <int OP, bool PAIR>
 struct GemmCfg {
   static constexpr bool kF4 = OP == kGemmFwd4;
@@ -725,43 +735,46 @@ __device__ void gemm_mma(const GroupedGemmParams& p, const GemmSmem& m, uint32_t
     const int kb = C::kWgrad ? walk.tile(p, m, 0).kb : p.K >> 5;
     if (kb == 0) continue;
     const int mmas = (kb * 32 + C::kMmaK - 1) / C::kMmaK;
-    // the tile whose columns this one takes: the last but one, or with
-    // overlapping accumulators the last
-    const int w = n - (C::kOverlap ? 1 : 2);
-    if (w >= 0 && !__all_sync(kFull, tc::spin(m.d_empty + (w & 1), (uint32_t)(w >> 1) & 1u))) {
-      if (leader) gemm_abort(p, m);
-      return;
-    }
-    tc::fence_after();
-    const uint32_t d = tbase + (uint32_t)((n & 1) * C::kAcc1);
-    for (int i0 = 0; i0 < mmas; i0 += 4) {
-      if (!__all_sync(kFull, tc::spin(m.full + slot, phase))) {
+    const int segment = p.out32 ? kSegment : mmas;
+    for (int i1 = 0; i1 < mmas; i1 += segment, ++n) {
+      // the tile (or segment) whose columns this one takes: the last but one,
+      // or with overlapping accumulators the last
+      const int w = n - (C::kOverlap ? 1 : 2);
+      if (w >= 0 && !__all_sync(kFull, tc::spin(m.d_empty + (w & 1), (uint32_t)(w >> 1) & 1u))) {
         if (leader) gemm_abort(p, m);
         return;
       }
       tc::fence_after();
-      if (leader) {
-        const uint64_t ad = a0 + (uint64_t)slot * (C::kStageBytes >> 4);
-        const uint64_t bd = b0 + (uint64_t)slot * (C::kStageBytes >> 4);
-        const uint32_t sf = tbase + C::kSfCol + slot * C::kSfPitch;
+      const uint32_t d = tbase + (uint32_t)((n & 1) * C::kAcc1);
+      const int end = min(mmas, i1 + segment);
+      for (int i0 = i1; i0 < end; i0 += 4) {
+        if (!__all_sync(kFull, tc::spin(m.full + slot, phase))) {
+          if (leader) gemm_abort(p, m);
+          return;
+        }
+        tc::fence_after();
+        if (leader) {
+          const uint64_t ad = a0 + (uint64_t)slot * (C::kStageBytes >> 4);
+          const uint64_t bd = b0 + (uint64_t)slot * (C::kStageBytes >> 4);
+          const uint32_t sf = tbase + C::kSfCol + slot * C::kSfPitch;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (i0 + j < mmas) {
-            const uint32_t id = C::kF4 ? (uint32_t)(j & 1) * 2 : (uint32_t)j;   // scale byte
-            const int word = C::kF4 ? j >> 1 : 0;
-            tc::mma<C::kCG, C::kF4>(d, ad + kStepA * j, bd + kStepB * j,
-                                    kIdesc | (id << 4) | (id << 29), sf + 4 * word,
-                                    sf + 4 * C::kWords + C::kSfbCols * word,
-                                    (i0 | j) != 0 ? 1u : 0u);
-          }
-        tc::commit<C::kCG>(m.empty + slot);
+          for (int j = 0; j < 4; ++j)
+            if (i0 + j < end) {
+              const uint32_t id = C::kF4 ? (uint32_t)(j & 1) * 2 : (uint32_t)j;   // scale byte
+              const int word = C::kF4 ? j >> 1 : 0;
+              tc::mma<C::kCG, C::kF4>(d, ad + kStepA * j, bd + kStepB * j,
+                                      kIdesc | (id << 4) | (id << 29), sf + 4 * word,
+                                      sf + 4 * C::kWords + C::kSfbCols * word,
+                                      i0 + j != i1 ? 1u : 0u);
+            }
+          tc::commit<C::kCG>(m.empty + slot);
+        }
+        __syncwarp();
+        if (++slot == C::kStages) slot = 0, phase ^= 1;
       }
+      if (leader) tc::commit<C::kCG>(m.d_full + (n & 1));
       __syncwarp();
-      if (++slot == C::kStages) slot = 0, phase ^= 1;
     }
-    if (leader) tc::commit<C::kCG>(m.d_full + (n & 1));
-    __syncwarp();
-    ++n;
   }
 }
 
@@ -769,26 +782,33 @@ __device__ void gemm_mma(const GroupedGemmParams& p, const GemmSmem& m, uint32_t
 // 32 rows x 128 bytes from registers (thread t: row t, as eight 16-byte
 // pieces) into the warp's staging, swizzled (piece c of row r at c ^ (r mod
 // 8)), and from there to the output: whole pieces by one bulk tensor store,
-// which clips columns past the output's and leaves the warp free; pieces with
-// fewer rows, and sums with what the output holds, by plain stores of whole
-// row segments.
+// which clips rows and columns past the output's and leaves the warp free; a
+// product's pieces with fewer rows by plain stores of whole row segments.
+// `add` (fp32): to what the output holds, by a bulk tensor addition in the
+// memory's own units (accumulating wgrad of 128 groups of 512 rows, 2048 x
+// 1536: 682 us, floor 528; loads, adds and plain stores by the warps: 1,050).
 template <bool WGRAD, bool OUT32>
 __device__ __forceinline__ void store_piece(const GroupedGemmParams& p, const void* tm_out,
                                             unsigned char* stg, const uint4* v,
                                             int64_t row, int rows, int col, int e, int e_row,
-                                            int lane) {
+                                            bool add, int lane) {
   constexpr int kPer = OUT32 ? 4 : 8;   // columns in 16 bytes
   if (lane == 0) tc::bulk_wait_read();   // the last store has read the staging
   __syncwarp();
 #pragma unroll
   for (int c = 0; c < 8; ++c)
     *reinterpret_cast<uint4*>(stg + lane * 128 + ((c ^ (lane & 7)) << 4)) = v[c];
-  if ((WGRAD || rows == 32) && !p.accumulate) {
+  if (WGRAD || rows == 32) {
     tc::fence_proxy_async();
     __syncwarp();
     if (lane == 0) {
-      if constexpr (WGRAD) tc::store_3d(tm_out, stg, col, e_row, e);
-      else tc::store_2d(tm_out, stg, col, (int)row);
+      if constexpr (WGRAD) {
+        if (OUT32 && add) tc::add_3d(tm_out, stg, col, e_row, e);
+        else tc::store_3d(tm_out, stg, col, e_row, e);
+      } else {
+        if (OUT32 && add) tc::add_2d(tm_out, stg, col, (int)row);
+        else tc::store_2d(tm_out, stg, col, (int)row);
+      }
       tc::bulk_commit();
     }
     __syncwarp();
@@ -797,6 +817,16 @@ __device__ __forceinline__ void store_piece(const GroupedGemmParams& p, const vo
   __syncwarp();
   const int c = lane & 7;
   const bool in = col + kPer * c < p.N;
+  float4 o[OUT32 ? 8 : 1];   // what the output holds: one wait for all of it
+  if constexpr (OUT32) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int r = 4 * k + (lane >> 3);
+      if (add && in && r < rows)
+        o[k] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.out) +
+                                                (row + r) * p.ldo + col + kPer * c);
+    }
+  }
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const int r = 4 * k + (lane >> 3);
@@ -807,11 +837,9 @@ __device__ __forceinline__ void store_piece(const GroupedGemmParams& p, const vo
                                                 col + kPer * c);
         float4 f = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z),
                                __uint_as_float(w.w));
-        if (p.accumulate) {
-          const float4 o = *dst;
-          f = make_float4(__fadd_rn(o.x, f.x), __fadd_rn(o.y, f.y), __fadd_rn(o.z, f.z),
-                          __fadd_rn(o.w, f.w));
-        }
+        if (add)
+          f = make_float4(__fadd_rn(o[k].x, f.x), __fadd_rn(o[k].y, f.y),
+                          __fadd_rn(o[k].z, f.z), __fadd_rn(o[k].w, f.w));
         *dst = f;
       } else {
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (row + r) * p.ldo + col +
@@ -836,9 +864,12 @@ __device__ void gemm_epilogue(const GroupedGemmParams& p, const GemmSmem& m, con
     const int rows = max(0, min(32, tile.rows - 32 * q));
     const int e_row = (int)tile.row0 + 32 * q;   // row of A, or (wgrad) of dW_e
     const int64_t row = (C::kWgrad ? (int64_t)tile.e * p.R : 0) + e_row;
+    const int mmas = (tile.kb * 32 + C::kMmaK - 1) / C::kMmaK;
+    const int segments = p.out32 ? (mmas + kSegment - 1) / kSegment : 1;
+    bool add = p.accumulate;
     auto put = [&](auto out32, const uint4* v, int col) {
       store_piece<C::kWgrad, decltype(out32)::value>(p, tm_out, stg, v, row, rows, col, tile.e,
-                                                     e_row, lane);
+                                                     e_row, add, lane);
     };
     using Bf16 = std::integral_constant<bool, false>;
     using Fp32 = std::integral_constant<bool, true>;
@@ -855,63 +886,65 @@ __device__ void gemm_epilogue(const GroupedGemmParams& p, const GemmSmem& m, con
       }
       continue;
     }
-    const int b = n & 1;
-    if (!__all_sync(kFull, tc::sleep(m.d_full + b, (uint32_t)(n >> 1) & 1u)) || gemm_aborted(m)) {
-      gemm_abort(p, m);
-      return;
-    }
-    tc::fence_after();
-    const uint32_t src = tbase + ((uint32_t)(32 * q) << 16) + (uint32_t)(b * C::kAcc1);
-    // The overlapping columns first: the first accumulator's last chunks, the
-    // second one's first.  The columns may be overwritten by the tile after the
-    // next once they are read here, and by the next one's where they overlap: a
-    // set without overlapping columns only says that it is through with the
-    // tile before this one.
-    constexpr int kOver = C::kOverlap / 64;
-    const bool over = C::kSets == 1 || (b == 0) == (set == 1);
-    auto release = [&]() {
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) tc::arrive_cluster(d_empty + 8 * b);
-    };
-    if (!over) release();
+    for (int seg = 0; seg < segments; ++seg, ++n, add = true) {
+      if (seg && lane == 0) tc::bulk_wait();   // the stores that it adds to are done
+      const int b = n & 1;
+      if (!__all_sync(kFull, tc::sleep(m.d_full + b, (uint32_t)(n >> 1) & 1u)) || gemm_aborted(m)) {
+        gemm_abort(p, m);
+        return;
+      }
+      tc::fence_after();
+      const uint32_t src = tbase + ((uint32_t)(32 * q) << 16) + (uint32_t)(b * C::kAcc1);
+      // The overlapping columns first: the first accumulator's last chunks, the
+      // second one's first.  The columns may be overwritten by the tile after the
+      // next once they are read here, and by the next one's where they overlap: a
+      // set without overlapping columns only says that it is through with the
+      // tile before this one.
+      constexpr int kOver = C::kOverlap / 64;
+      const bool over = C::kSets == 1 || (b == 0) == (set == 1);
+      auto release = [&]() {
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::arrive_cluster(d_empty + 8 * b);
+      };
+      if (!over) release();
 #pragma unroll 1
-    for (int i = 0; i < kChunks; ++i) {
-      const int c = kChunks * set +
-                    (kOver && b == 0 && over ? (i + kChunks - kOver) % kChunks : i);
-      uint32_t v[64];
-      tc::ld32(src + 64 * c, v);
-      tc::ld32(src + 64 * c + 32, v + 32);
-      tc::wait_ld();
-      tc::tie(v);
-      tc::tie(v + 32);
-      if (over && i == (kOver ? kOver : kChunks) - 1) release();
-      const int col = tile.n0 + 64 * c;
-      if (col >= p.N || rows == 0) continue;
-      if (p.out32) {
+      for (int i = 0; i < kChunks; ++i) {
+        const int c = kChunks * set +
+                      (kOver && b == 0 && over ? (i + kChunks - kOver) % kChunks : i);
+        uint32_t v[64];
+        tc::ld32(src + 64 * c, v);
+        tc::ld32(src + 64 * c + 32, v + 32);
+        tc::wait_ld();
+        tc::tie(v);
+        tc::tie(v + 32);
+        if (over && i == (kOver ? kOver : kChunks) - 1) release();
+        const int col = tile.n0 + 64 * c;
+        if (col >= p.N || rows == 0) continue;
+        if (p.out32) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < 2; ++h) {
+            uint4 w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              w[j] = make_uint4(v[32 * h + 4 * j], v[32 * h + 4 * j + 1], v[32 * h + 4 * j + 2],
+                                v[32 * h + 4 * j + 3]);
+            if (col + 32 * h < p.N) put(Fp32(), w, col + 32 * h);
+          }
+        } else {
           uint4 w[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            w[j] = make_uint4(v[32 * h + 4 * j], v[32 * h + 4 * j + 1], v[32 * h + 4 * j + 2],
-                              v[32 * h + 4 * j + 3]);
-          if (col + 32 * h < p.N) put(Fp32(), w, col + 32 * h);
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t* x = v + 8 * j;
+            w[j] = make_uint4(pack_bf16x2(__uint_as_float(x[0]), __uint_as_float(x[1])),
+                              pack_bf16x2(__uint_as_float(x[2]), __uint_as_float(x[3])),
+                              pack_bf16x2(__uint_as_float(x[4]), __uint_as_float(x[5])),
+                              pack_bf16x2(__uint_as_float(x[6]), __uint_as_float(x[7])));
+          }
+          put(Bf16(), w, col);
         }
-      } else {
-        uint4 w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t* x = v + 8 * j;
-          w[j] = make_uint4(pack_bf16x2(__uint_as_float(x[0]), __uint_as_float(x[1])),
-                            pack_bf16x2(__uint_as_float(x[2]), __uint_as_float(x[3])),
-                            pack_bf16x2(__uint_as_float(x[4]), __uint_as_float(x[5])),
-                            pack_bf16x2(__uint_as_float(x[6]), __uint_as_float(x[7])));
-        }
-        put(Bf16(), w, col);
       }
     }
-    ++n;
   }
   if (lane == 0) tc::bulk_wait();   // the stores are out before the memory is given up
   __syncwarp();

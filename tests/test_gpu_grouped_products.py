@@ -160,6 +160,70 @@ def test_wgrad_accumulates(cuda_device):
     assert torch.equal(out, held + once)         # one fp32 addition
 
 
+def test_wgrad_accumulates_long_sums(cuda_device):
+    splits, H, K = [8193, 0, 20011, 31, 8192, 9000], 1312, 288
+    dy, x, sy, sx, ro, cb, want, size = _wgrad_case(splits, H, K, 42)
+    out = torch.randn(want.shape, generator=_gen(2), device="cuda")
+    want, size = want + out.double(), size + out.double().abs()
+    a, b = mg.MXFP8(None, dy, None, sy), mg.MXFP8(None, x, None, sx)
+    mg.grouped_mxfp8_wgrad(a, b, ro, cb, out=out, accumulate=True)
+    _check(out, want, size, max(splits), "accumulate")
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("splits", [[1, 0, 17], [300, 0, 2000, 130]])
+@pytest.mark.parametrize("op", ["gemm", "dgrad", "gemm4"])
+def test_long_row_sums(cuda_device, op, splits, out_dtype):
+    K, H = (2592, 16480) if op == "dgrad" else (16480, 2592)
+    call, want, size, n, _, _ = _rows_case(op, splits, K, H, 60)
+    out, status = call(out_dtype=out_dtype)
+    assert int(status) == 0
+    _check(out, want, size, n, (op, splits))
+
+
+@pytest.mark.parametrize("rows,cols", [(65536, 128), (65519, 128), (65536, 2048)])
+@pytest.mark.parametrize("op", ["wgrad", "gemm", "dgrad", "gemm4"])
+def test_long_sums_keep_small_terms(cuda_device, op, rows, cols):
+    """A sum over `rows` products of 2^23 (the first block) and 2^-5 for every
+    other block.  In fp32 beside 2^23 a term of 2^-5 is 1/32 of a step and may
+    vanish.  Sums in segments of 256 steps (of 32 products, MXFP4: 64) lose
+    those of the first segment, at most 256 / 32 = 8 (MXFP4: 512 / 32 = 16);
+    later ones are sums of at most 16, exact by themselves, and each is added
+    with at most half a step of 2^23, 0.5, for 7 (MXFP4: 3) of them: 11.5
+    (17.5).  One sum would lose up to 64, all of them."""
+    if op != "wgrad" and rows % 32:
+        pytest.skip("the summed index is whole blocks there")
+    nb, m = (rows + 31) // 32, cols if op == "wgrad" else min(cols, 1600)
+    ones8 = lambda *s: torch.full(s, 0x38, dtype=torch.uint8, device="cuda")
+    ones4 = lambda *s: torch.full(s, 0x22, dtype=torch.uint8, device="cuda")
+    scale = lambda *s: torch.full(s, 127, dtype=torch.uint8, device="cuda")
+    exps = torch.full((nb,), 127 - 10, dtype=torch.uint8, device="cuda")
+    exps[0] = 127 + 18
+    byrow = exps.expand(m, nb).contiguous()
+    ro = _dev([0, m])
+    if op == "wgrad":
+        dy = mg.MXFP8(None, ones8(rows, m), None, exps[:, None].expand(nb, m).contiguous())
+        x = mg.MXFP8(None, ones8(rows, cols), None, scale(nb, cols))
+        out, status = mg.grouped_mxfp8_wgrad(dy, x, _dev([0, rows]), _dev([0, nb]))
+    elif op == "gemm":
+        out, status = mg.grouped_mxfp8_gemm(
+            mg.MXFP8(ones8(m, rows), None, byrow, None),
+            mg.MXFP8(ones8(cols, rows), None, scale(cols, nb), None), ro, out_dtype=torch.float32)
+    elif op == "dgrad":
+        out, status = mg.grouped_mxfp8_dgrad(
+            mg.MXFP8(ones8(m, rows), None, byrow, None),
+            mg.MXFP8(None, ones8(rows, cols), None, scale(nb, cols)), ro, out_dtype=torch.float32)
+    else:
+        out, status = mg.grouped_mxfp4_gemm(
+            mg.MXFP4(ones4(m, rows // 2), byrow),
+            mg.MXFP4(ones4(cols, rows // 2), scale(cols, nb)), ro, out_dtype=torch.float32)
+    assert int(status) == 0
+    last = rows - 32 * (nb - 1)
+    want = 2.0 ** 23 + (nb - 2) / 32 + last / 1024
+    err = (out.double() - want).abs().max().item()
+    assert err <= (17.5 if op == "gemm4" else 11.5), err
+
+
 @pytest.mark.parametrize("splits", [[128, 0, 256], [1280, 128, 640]])
 def test_tiled_scales(cuda_device, splits):
     """Scales in the GEMM-ready layout give the row-major ones' bits."""
