@@ -435,6 +435,8 @@ __device__ __forceinline__ int scale_mode(bool outer, bool tiled, int pitch) {
          : pitch <= 4 * kChunk ? kFlat
          : (pitch & 3) == 0 ? kRows4 : kRowsAny;
 }
+// Whether the copies go by a tensor map (else there is none).
+__device__ __forceinline__ bool scales_by_map(int mode) { return mode == kRows16 || mode == kCols; }
 
 // What put_chunk needs of a chunk of a group: its words (4 bits), the place of
 // its first byte in the 16 or 4 bytes copied first (4 bits), the bytes of a row
@@ -981,11 +983,13 @@ __global__ void __launch_bounds__(GemmCfg<OP, PAIR>::kThreads, 1)
   m.pre = reinterpret_cast<int*>(reinterpret_cast<unsigned char*>(bars) + kGemmMisc);
   m.ro = p.E <= kGroupsInSmem ? m.pre + p.E + 1 : nullptr;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
-    tc::prefetch_map(&tm_a);
-    tc::prefetch_map(&tm_b);
-    if (!p.a_tiled) tc::prefetch_map(&tm_sa);
-    if (!p.b_tiled) tc::prefetch_map(&tm_sb);
+  if (tid == 0) {   // only the maps that the host has encoded: those that copies will use
+    if (p.M > 0) {
+      tc::prefetch_map(&tm_a);
+      tc::prefetch_map(&tm_b);
+      if (scales_by_map(scale_mode(C::kAmn, p.a_tiled, p.K >> 5))) tc::prefetch_map(&tm_sa);
+      if (scales_by_map(scale_mode(C::kBmn, p.b_tiled, p.K >> 5))) tc::prefetch_map(&tm_sb);
+    }
     tc::prefetch_map(&tm_out);
   }
   const int rank = PAIR ? (int)tc::cluster_rank() : 0;
