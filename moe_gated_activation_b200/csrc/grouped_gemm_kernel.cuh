@@ -16,7 +16,6 @@
 //   warp 8     TMA loads of the code tiles (128 rows x 128 bytes each);
 //   warp 9     tensor-memory allocation; in the pair's first SM the MMAs;
 //   warp 10    the scales' copies into shared memory, some chunks ahead;
-//   warp 11    wgrad: clears the rows past a group's end;
 //   warps 12-15  wgrad on pairs: a second set of epilogue warps.
 // One ring of stages carries codes and scales: `full` collects the TMA bytes
 // and the scale warps of both SMs, `empty` comes from the MMAs' commit.
@@ -71,8 +70,12 @@ struct GemmCfg {
   // wgrad on pairs: short sums, so a second set of epilogue warps (12-15) takes
   // half of the columns
   static constexpr int kSets = PAIR && kWgrad ? 2 : 1;
-  static constexpr int kThreads = kSets == 2 ? 512 : kWgrad ? 384 : 352;
+  static constexpr int kThreads = kSets == 2 ? 512 : 352;
   static constexpr int kCG = PAIR ? 2 : 1;
+  // Of the handovers between a pair's SMs only that of a stage to the MMAs has
+  // shared memory behind it, which the copies write.
+  static constexpr tc::Order kOrder = PAIR ? tc::kPair : tc::kSm;
+  static constexpr tc::Order kDataOrder = PAIR ? tc::kPairData : tc::kSm;
   static constexpr int kTM = 128 * kCG;
   static constexpr int kBN = PAIR ? 256 : 128;
   // (the second set's staging takes the place of a fifth stage)
@@ -106,7 +109,6 @@ struct GemmSmem {
   unsigned char* sf;   // [kChunk][A's rows, B's rows by 128][512] scale words
   unsigned char* raw;  // [groups][kRawDepth][kRawBytes] the same as they arrive
   uint64_t* full;      // [kStages] (first SM of a pair) codes and scales are in
-  uint64_t* landed;    // [kStages] wgrad: this SM's codes are in, group ends not yet cleared
   uint64_t* empty;     // [kStages] the stage's MMAs are done
   uint64_t* raw_full;  // [groups][kRawDepth] a chunk of scales has arrived
   uint64_t* raw_empty; // [kRawDepth] ... and is in its pieces
@@ -465,7 +467,7 @@ __device__ void gemm_scale_loader(const GroupedGemmParams& p, const GemmSmem& m,
     const GemmTile t = w.tile(p, m, rank);
     const int words = (t.kb + 3) >> 2;
     for (int u = 0; u < words; u += kChunk) {
-      if (!__all_sync(kFull, tc::sleep(m.raw_empty + buf, phase)) || gemm_aborted(m)) {
+      if (!__all_sync(kFull, tc::sleep<tc::kSm>(m.raw_empty + buf, phase)) || gemm_aborted(m)) {
         gemm_abort(p, m);
         return;
       }
@@ -506,7 +508,7 @@ __device__ void gemm_scale_loader(const GroupedGemmParams& p, const GemmSmem& m,
     }
   }
   // the end: a chunk without stages
-  if (!__all_sync(kFull, tc::sleep(m.raw_empty + buf, phase)) || gemm_aborted(m)) {
+  if (!__all_sync(kFull, tc::sleep<tc::kSm>(m.raw_empty + buf, phase)) || gemm_aborted(m)) {
     gemm_abort(p, m);
     return;
   }
@@ -534,7 +536,7 @@ __device__ __forceinline__ void gemm_scales(const GroupedGemmParams& p, const Ge
   uint32_t raw_phase = 0;
   const int pitch = p.K >> 5;
   auto serve = [&](int buf) {
-    bool ok = __all_sync(kFull, tc::sleep(raw_full + buf, raw_phase));
+    bool ok = __all_sync(kFull, tc::sleep<tc::kSm>(raw_full + buf, raw_phase));
     int stages = 0;
     if (ok) {
       stages = *reinterpret_cast<volatile int*>(m.head + 4 * buf);
@@ -564,7 +566,7 @@ __device__ __forceinline__ void gemm_scales(const GroupedGemmParams& p, const Ge
     };
     if (stages > 0) read(0);
     for (int s = 0; s < stages; ++s) {
-      ok = ok && __all_sync(kFull, tc::spin(m.empty + slot, phase));
+      ok = ok && __all_sync(kFull, tc::spin<C::kOrder>(m.empty + slot, phase));
       if (ok) {
         tc::fence_after();
         const uint32_t dst = dst0 + slot * C::kSfPitch;
@@ -579,7 +581,7 @@ __device__ __forceinline__ void gemm_scales(const GroupedGemmParams& p, const Ge
         tc::wait_st();
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::arrive_cluster(full0 + 8 * slot);
+        if (lane == 0) tc::arrive_leader<C::kOrder>(full0 + 8 * slot);
       }
       if (s + 1 < stages) read(s + 1);
       if (++slot == C::kStages) slot = 0, phase ^= 1;
@@ -628,45 +630,59 @@ __device__ __forceinline__ void gemm_scales_any(const GroupedGemmParams& p, cons
 }
 
 // ------------------------------------------------------------ code tiles
-// Warp 8.
+// Warp 8.  wgrad: blocks of 32 rows of a group at any row.  The rows past the
+// group's end are the next group's: they must not meet in the sum, and a zero
+// times a NaN of theirs would not be zero, so they are zeros in both operands.
+// The copies put them there: the maps are [rows][32][columns], row z's 32 next
+// rows, and a box that starts `32 - r` rows before them is filled with that many
+// zeros, then the r rows.  (Both operands' rows move alike, so the sum is the
+// same.  A warp that cleared the rows after the copies had to order its stores
+// between the SMs of a pair: a release to the pair in every tile, wgrad train
+// 456 us for 417.)
 template <typename C>
 __device__ __forceinline__ void gemm_copy_codes(const GroupedGemmParams& p, const GemmSmem& m,
                                                 const void* tm_a, const void* tm_b, int tiles,
                                                 int first, int step, int rank) {
-  // wgrad's copies complete on barriers of this SM's: gemm_clear passes them on
-  const uint32_t bar0 = C::kAmn ? smem_addr(m.landed) : tc::leader_addr(m.full);
+  const uint32_t full0 = tc::leader_addr(m.full);
   int slot = 0;
   uint32_t phase = 1;
   for (GemmWalk<C> walk(p, first, step, tiles); !walk.done(); walk.next()) {
     const GemmTile tile = walk.tile(p, m, rank);
     const int stages = (tile.kb * 32 + C::kStageK - 1) / C::kStageK;
     const int col_b = tile.n0 + (C::kCG == 2 ? 128 * rank : 0);   // this SM's rows of B
-    // the boxes' rows: of the summed index where that is outermost
-    const int ya = C::kAmn ? (int)tile.k0 : (int)tile.row0;
-    const int yb = C::kAmn ? (int)tile.k0 : C::kBmn ? tile.e * p.K : tile.e * p.N + col_b;
+    // B's first box row: of the summed index where that is outermost
+    const int yb = C::kBmn ? tile.e * p.K : tile.e * p.N + col_b;
     const int rows_a = (tile.rows + C::kABox - 1) / C::kABox;
     for (int s = 0; s < stages; ++s) {
-      if (!tc::spin(m.empty + slot, phase)) {
+      if (!tc::spin<C::kOrder>(m.empty + slot, phase)) {
         gemm_abort(p, m);
         return;
       }
       unsigned char* da = m.stages + slot * C::kStageBytes;
       unsigned char* db = da + kTileBytes;
-      const uint32_t bar = bar0 + 8 * slot;
+      const uint32_t bar = full0 + 8 * slot;
       const int blocks = min(4, tile.kb - 4 * s);
       const int na = C::kAmn ? blocks : rows_a, nb = C::kBmn ? blocks : 1;
       const uint32_t bytes = (uint32_t)(na * C::kABox + nb * C::kBBox) * 128u;
-      if constexpr (C::kAmn || C::kCG == 1)
+      if constexpr (C::kCG == 1)
         tc::arrive_tx(bar, bytes);
       else
-        tc::arrive_tx_cluster(bar, bytes);
-      constexpr int kLoad = C::kAmn ? 1 : C::kCG;
-      for (int i = 0; i < na; ++i)
-        tc::load_2d<kLoad>(da + i * C::kABox * 128, tm_a, C::kAmn ? (int)tile.row0 : 128 * s,
-                           ya + (C::kAmn ? 128 * s : 0) + C::kABox * i, bar);
-      for (int i = 0; i < nb; ++i)
-        tc::load_2d<kLoad>(db + i * C::kBBox * 128, tm_b, C::kBmn ? col_b : 128 * s,
-                           yb + (C::kBmn ? 128 * s : 0) + C::kBBox * i, bar);
+        tc::arrive_tx_leader(bar, bytes);
+      if constexpr (C::kWgrad) {
+        for (int i = 0; i < blocks; ++i) {
+          const int row = 32 * (4 * s + i), y = min(0, tile.krows - row - 32);
+          tc::load_3d<C::kCG>(da + i * C::kABox * 128, tm_a, (int)tile.row0, y,
+                              (int)tile.k0 + row, bar);
+          tc::load_3d<C::kCG>(db + i * C::kBBox * 128, tm_b, col_b, y, (int)tile.k0 + row, bar);
+        }
+      } else {
+        for (int i = 0; i < na; ++i)
+          tc::load_2d<C::kCG>(da + i * C::kABox * 128, tm_a, 128 * s,
+                              (int)tile.row0 + C::kABox * i, bar);
+        for (int i = 0; i < nb; ++i)
+          tc::load_2d<C::kCG>(db + i * C::kBBox * 128, tm_b, C::kBmn ? col_b : 128 * s,
+                              yb + (C::kBmn ? 128 * s : 0) + C::kBBox * i, bar);
+      }
       if (++slot == C::kStages) slot = 0, phase ^= 1;
     }
   }
@@ -679,39 +695,6 @@ __device__ void gemm_producer(const GroupedGemmParams& p, const GemmSmem& m, con
                               const void* tm_b, int tiles, int first, int step, int rank) {
   if (tc::elect_one()) gemm_copy_codes<C>(p, m, tm_a, tm_b, tiles, first, step, rank);
   __syncwarp();
-}
-
-// Warp 11, wgrad: once a stage has landed, clears the rows past the group's end
-// in its last block of 32 -- in both operands: the next group's rows must not
-// meet in the sum, and a zero times a NaN of theirs would not be zero -- and
-// passes the stage on to the MMAs.
-template <typename C>
-__device__ void gemm_clear(const GroupedGemmParams& p, const GemmSmem& m, int tiles, int first,
-                           int step, int rank) {
-  const int lane = threadIdx.x & 31;
-  int slot = 0;
-  uint32_t phase = 0;
-  for (GemmWalk<C> walk(p, first, step, tiles); !walk.done(); walk.next()) {
-    const GemmTile tile = walk.tile(p, m, rank);
-    for (int left = tile.krows; left > 0; left -= 128) {
-      if (!__all_sync(kFull, tc::spin(m.landed + slot, phase))) {
-        gemm_abort(p, m);
-        return;
-      }
-      if (left < 128 && (left & 31) != 0) {
-        unsigned char* a = m.stages + slot * C::kStageBytes + left * 128;
-        const int n = (32 - (left & 31)) * 8;   // 16-byte pieces
-        for (int i = lane; i < n; i += 32) {
-          reinterpret_cast<uint4*>(a)[i] = make_uint4(0u, 0u, 0u, 0u);
-          reinterpret_cast<uint4*>(a + kTileBytes)[i] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        tc::fence_proxy_async();
-      }
-      __syncwarp();
-      if (lane == 0) tc::arrive_cluster(tc::leader_addr(m.full + slot));
-      if (++slot == C::kStages) slot = 0, phase ^= 1;
-    }
-  }
 }
 
 // ------------------------------------------------------------ MMAs
@@ -742,7 +725,8 @@ __device__ void gemm_mma(const GroupedGemmParams& p, const GemmSmem& m, uint32_t
       // the tile (or segment) whose columns this one takes: the last but one,
       // or with overlapping accumulators the last
       const int w = n - (C::kOverlap ? 1 : 2);
-      if (w >= 0 && !__all_sync(kFull, tc::spin(m.d_empty + (w & 1), (uint32_t)(w >> 1) & 1u))) {
+      if (w >= 0 && !__all_sync(kFull, tc::spin<C::kOrder>(m.d_empty + (w & 1),
+                                                              (uint32_t)(w >> 1) & 1u))) {
         if (leader) gemm_abort(p, m);
         return;
       }
@@ -750,7 +734,7 @@ __device__ void gemm_mma(const GroupedGemmParams& p, const GemmSmem& m, uint32_t
       const uint32_t d = tbase + (uint32_t)((n & 1) * C::kAcc1);
       const int end = min(mmas, i1 + segment);
       for (int i0 = i1; i0 < end; i0 += 4) {
-        if (!__all_sync(kFull, tc::spin(m.full + slot, phase))) {
+        if (!__all_sync(kFull, tc::spin<C::kDataOrder>(m.full + slot, phase))) {
           if (leader) gemm_abort(p, m);
           return;
         }
@@ -891,7 +875,7 @@ __device__ void gemm_epilogue(const GroupedGemmParams& p, const GemmSmem& m, con
     for (int seg = 0; seg < segments; ++seg, ++n, add = true) {
       if (seg && lane == 0) tc::bulk_wait();   // the stores that it adds to are done
       const int b = n & 1;
-      if (!__all_sync(kFull, tc::sleep(m.d_full + b, (uint32_t)(n >> 1) & 1u)) || gemm_aborted(m)) {
+      if (!__all_sync(kFull, tc::sleep<C::kOrder>(m.d_full + b, (uint32_t)(n >> 1) & 1u)) || gemm_aborted(m)) {
         gemm_abort(p, m);
         return;
       }
@@ -907,7 +891,7 @@ __device__ void gemm_epilogue(const GroupedGemmParams& p, const GemmSmem& m, con
       auto release = [&]() {
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::arrive_cluster(d_empty + 8 * b);
+        if (lane == 0) tc::arrive_leader<C::kOrder>(d_empty + 8 * b);
       };
       if (!over) release();
 #pragma unroll 1
@@ -971,8 +955,7 @@ __global__ void __launch_bounds__(GemmCfg<OP, PAIR>::kThreads, 1)
   m.raw = m.sf + C::kSfBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(m.raw + C::kGroups * C::kRawGroupBytes);
   m.full = bars;
-  m.landed = m.full + C::kStages;
-  m.empty = m.landed + C::kStages;
+  m.empty = m.full + C::kStages;
   m.raw_full = m.empty + C::kStages;
   m.raw_empty = m.raw_full + C::kGroups * kRawDepth;
   m.d_full = m.raw_empty + kRawDepth;
@@ -1047,8 +1030,7 @@ __global__ void __launch_bounds__(GemmCfg<OP, PAIR>::kThreads, 1)
   // ---- barriers and tensor memory
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(m.full + i, 5 * C::kCG);   // per SM: warp 8 (wgrad: 11) and four scale warps
-      mbar_init(m.landed + i, 1);
+      mbar_init(m.full + i, 5 * C::kCG);   // per SM: warp 8 and four scale warps
       mbar_init(m.empty + i, 1);
     }
     for (int i = 0; i < C::kGroups * kRawDepth; ++i) mbar_init(m.raw_full + i, 32);
@@ -1075,7 +1057,6 @@ __global__ void __launch_bounds__(GemmCfg<OP, PAIR>::kThreads, 1)
   else if (warp < 8) gemm_scales_any<C>(p, m, tbase, warp - 4);
   else if (warp == 8) gemm_producer<C>(p, m, &tm_a, &tm_b, tiles, first, step, rank);
   else if (warp == 10) gemm_scale_loader<C>(p, m, &tm_sa, &tm_sb, tiles, first, step, rank);
-  else if (C::kWgrad && warp == 11) gemm_clear<C>(p, m, tiles, first, step, rank);
   else if (warp == 9 && rank == 0) gemm_mma<C>(p, m, tbase, tiles, first, step);
 
   tc::fence_before();

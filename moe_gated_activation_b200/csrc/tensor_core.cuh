@@ -137,20 +137,32 @@ __device__ __forceinline__ uint32_t leader_addr(const void* p) {
 __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
-// Arrivals on a barrier of the pair's first SM (bar: its cluster address).
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar)
-               : "memory");
+// What an arrival on a barrier and the wait for it order.
+enum Order : int {
+  kSm,        // everything, between threads of one SM
+  kPair,      // between the SMs of a pair, tensor memory only (fence_before before
+              // the arrival, fence_after after the wait): no memory is handed over
+  kPairData,  // a wait, between the SMs of a pair: also what their copies wrote
+};
+
+// An arrival on a barrier of the pair's first SM (bar: its cluster address).
+template <Order O>
+__device__ __forceinline__ void arrive_leader(uint32_t bar) {
+  if constexpr (O == kSm)
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  else
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+                 : "memory");
 }
 __device__ __forceinline__ void arrive_tx(uint32_t bar, uint32_t bytes) {   // this SM's
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ void arrive_tx_cluster(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;"
+__device__ __forceinline__ void arrive_tx_leader(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;"
                ::"r"(bar), "r"(bytes) : "memory");
 }
-// 2-D tile load into this SM's shared memory, completing on the barrier at
+// Tile loads into this SM's shared memory, completing on the barrier at
 // cluster address `bar` (this SM's, or with CG = 2 the pair's first SM's).
 template <int CG>
 __device__ __forceinline__ void load_2d(void* dst, const void* tmap, int x, int y, uint32_t bar) {
@@ -165,6 +177,24 @@ __device__ __forceinline__ void load_2d(void* dst, const void* tmap, int x, int 
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
         "bytes [%0], [%1, {%2, %3}], [%4];"
         ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void load_3d(void* dst, const void* tmap, int x, int y, int z,
+                                        uint32_t bar) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z),
+        "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
+        "bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z),
+        "r"(bar)
         : "memory");
 }
 
@@ -211,36 +241,40 @@ __device__ __forceinline__ void bulk_wait() {
 
 // Bounded waits (the global timer, one second).  spin: without suspending,
 // for the single warps that feed the tensor cores, whose wake-up latency
-// counts.  Both order what other SMs of the cluster released before arriving.
-__device__ __forceinline__ bool test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, "
-               "[%1], %2; selp.u32 %0, 1, 0, p; }"
-               : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool test_sleep(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, "
-               "[%1], %2, %3; selp.u32 %0, 1, 0, p; }"
-               : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity), "r"(kWaitHintNs) : "memory");
-  return ok != 0;
-}
+// counts.
+#define MOEACT_WAIT_FORM(NAME, FORM, HINT)                                              \
+  template <Order O>                                                                    \
+  __device__ __forceinline__ bool NAME(uint64_t* bar, uint32_t parity) {                \
+    uint32_t ok;                                                                        \
+    if constexpr (O == kSm) MOEACT_WAIT_ASM(FORM "shared::cta.b64", HINT);              \
+    else if constexpr (O == kPair) MOEACT_WAIT_ASM(FORM "relaxed.cluster.shared::cta.b64", HINT); \
+    else MOEACT_WAIT_ASM(FORM "acquire.cluster.shared::cta.b64", HINT);                 \
+    return ok != 0;                                                                     \
+  }
+#define MOEACT_WAIT_ASM(FORM, HINT)                                                      \
+  asm volatile("{ .reg .pred p; " FORM " p, [%1], %2" HINT "; selp.u32 %0, 1, 0, p; }"   \
+               : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity), "r"(kWaitHintNs) : "memory")
+MOEACT_WAIT_FORM(test, "mbarrier.test_wait.parity.", "")
+MOEACT_WAIT_FORM(test_sleep, "mbarrier.try_wait.parity.", ", %3")
+#undef MOEACT_WAIT_FORM
+#undef MOEACT_WAIT_ASM
+template <Order O>
 __device__ __forceinline__ bool spin(uint64_t* bar, uint32_t parity) {
-  if (test(bar, parity)) return true;
+  if (test<O>(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   for (;;) {
     for (int i = 0; i < 64; ++i)
-      if (test(bar, parity)) return true;
+      if (test<O>(bar, parity)) return true;
     if (global_ns() - t0 > kWaitLimitNs) return false;
   }
 }
+template <Order O>
 __device__ __forceinline__ bool sleep(uint64_t* bar, uint32_t parity) {
-  if (test_sleep(bar, parity)) return true;
+  if (test_sleep<O>(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   for (;;) {
     for (int i = 0; i < 4; ++i)
-      if (test_sleep(bar, parity)) return true;
+      if (test_sleep<O>(bar, parity)) return true;
     if (global_ns() - t0 > kWaitLimitNs) return false;
   }
 }

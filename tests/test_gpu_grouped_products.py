@@ -291,6 +291,28 @@ def test_nan_stays_in_its_group(cuda_device, splits, K, H):
     _check(dw[keep], want[keep], size[keep], max(splits), "wgrad")
 
 
+@pytest.mark.parametrize("seed", range(4))
+def test_nan_after_every_group_end(cuda_device, seed):
+    """wgrad on pairs: every other group is NaN and every group ends inside a
+    block of 32, whose remaining rows, the next group's, take no part in either
+    SM of a pair."""
+    g = torch.Generator().manual_seed(seed)
+    splits = [int(m) for m in torch.randint(1, 180, (64,), generator=g)]
+    splits = [m + (m % 32 == 0) for m in splits]
+    H, K = 544, 512
+    dy, x, sy, sx, ro, cb, want, size = _wgrad_case(splits, H, K, 20 + seed)
+    offs, blocks = _offs(splits), _blocks(splits)
+    for e in range(1, 64, 2):
+        for t, s in ((dy, sy), (x, sx)):
+            t[offs[e]:offs[e + 1]] = 0x7F
+            s[blocks[e]:blocks[e + 1]] = 255
+    for _ in range(8):
+        dw, st = mg.grouped_mxfp8_wgrad(mg.MXFP8(None, dy, None, sy), mg.MXFP8(None, x, None, sx),
+                                        ro, cb)
+        assert int(st) == 0 and bool(dw[1::2].isnan().all())
+        _check(dw[::2], want[::2], size[::2], max(splits), splits)
+
+
 def test_extreme_scales(cuda_device):
     """Scales whose product leaves fp32's range overflow to infinity and
     vanish to zero; 2^-127 times 2^127 is one."""
