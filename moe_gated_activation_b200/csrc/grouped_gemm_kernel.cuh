@@ -304,6 +304,8 @@ __device__ __forceinline__ void start_chunk(const ScaleSrc& c, const void* tmap,
     if (lane == 0) {   // the rows are a tile's: its words lie one after another
       const int64_t tile = OUTER ? c.tile0 : (c.r0 >> 7) * c.words;
       mbar_expect_tx(bar, 512 * n);
+      // the buffer's last chunk may have come by cp.async (another group's rows)
+      if constexpr (!OUTER) tc::fence_proxy_async();
       if (n > 0) bulk_load(raw, c.s + ((tile + u) << 9), 512 * n, bar);
       return;
     }

@@ -255,6 +255,32 @@ def test_tiled_scales(cuda_device, splits):
     assert int(st) == 0 and torch.equal(got, plain)
 
 
+@pytest.mark.parametrize("K", [384, 1280])
+@pytest.mark.parametrize("splits", [[5, 123, 0, 130, 126], [128, 3, 125, 256, 1, 127] * 3,
+                                    [128, 700, 129, 1, 322, 1280], [640, 641, 1, 639, 639]])
+@pytest.mark.parametrize("op", ["gemm", "dgrad", "gemm4"])
+def test_tiled_scales_of_ragged_groups(cuda_device, op, splits, K):
+    """The row products take tiled scales of groups that start anywhere in a
+    tile: groups at a tile's start and inside one, in one launch, on single SMs
+    and on pairs, give the row-major scales' bits."""
+    H = 2560
+    call, want, size, n, _, (a, sa, w, sw, ro) = _rows_case(
+        op, splits, *((H, K) if op == "dgrad" else (K, H)), 30)
+    plain, _ = call()
+    _check(plain, want, size, n, (op, splits))
+    ta = ref.tile_scales(sa)
+    for _ in range(4):
+        if op == "gemm4":
+            got, st = mg.grouped_mxfp4_gemm(mg.MXFP4(a, ta), mg.MXFP4(w, sw), ro, gemm_scales=True)
+        elif op == "gemm":
+            got, st = mg.grouped_mxfp8_gemm(mg.MXFP8(a, None, ta, None),
+                                            mg.MXFP8(w, None, sw, None), ro, gemm_scales=True)
+        else:
+            got, st = mg.grouped_mxfp8_dgrad(mg.MXFP8(a, None, ta, None),
+                                             mg.MXFP8(None, w, None, sw), ro, gemm_scales=True)
+        assert int(st) == 0 and torch.equal(got, plain)
+
+
 def test_tiled_scales_need_whole_groups(cuda_device):
     dy, x, sy, sx, ro, cb, _, _ = _wgrad_case([64, 64], 128, 128, 4)
     out = torch.full((2, 128, 128), 7.0, device="cuda")
