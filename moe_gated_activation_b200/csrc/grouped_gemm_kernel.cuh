@@ -269,11 +269,11 @@ __device__ __forceinline__ ScaleSrc scale_src(const GroupedGemmParams& p, const 
   return r;
 }
 
-__device__ __forceinline__ void copy4(uint32_t dst, const uint8_t* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+// `have` bytes (1 .. 4; 1 .. 16) and zeros to 4 (16).
+__device__ __forceinline__ void copy4(uint32_t dst, const uint8_t* src, int have = 4) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(have)
+               : "memory");
 }
-
-// `have` bytes (1 .. 16) and zeros to 16.
 __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, int have) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have)
                : "memory");
@@ -328,14 +328,14 @@ __device__ __forceinline__ void start_chunk(const ScaleSrc& c, const void* tmap,
       }
     } else {
       // up to nine words a row, neighbouring lanes a row's (kRowsAny: aligned
-      // words that hold its eight; the array starts on a word, and a word that
-      // holds one of its bytes is read whole)
+      // words that hold its eight; of the array's last word the bytes that are
+      // the array's)
       constexpr int kPer = MODE == kRowsAny ? 9 : 8;
-      const int64_t end = (c.bytes - 1) >> 2;
       for (int t = lane; t < kPer * rows; t += 32) {
         const int r = t / kPer, i = t - kPer * r;
-        const int64_t at = ((c.r0 + r) * c.pitch + 4 * u) >> 2;
-        if (i < n + kPer - 8) copy4(dst + 36 * r + 4 * i, c.s + 4 * min(at + i, end));
+        const int64_t at = (((c.r0 + r) * c.pitch + 4 * u) & ~(int64_t)3) + 4 * i;
+        if (i < n + kPer - 8 && at < c.bytes)
+          copy4(dst + 36 * r + 4 * i, c.s + at, (int)min((int64_t)4, c.bytes - at));
       }
     }
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))

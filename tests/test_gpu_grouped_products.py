@@ -524,6 +524,27 @@ def test_scales_and_codes_at_the_end_of_their_memory(cuda_device):
     _check(out, want, size, n, "inside")
 
 
+@pytest.mark.parametrize("rows", [[1], [20, 17], [128, 0, 131], [1030, 0, 901]])
+@pytest.mark.parametrize("op", ["gemm", "dgrad", "gemm4"])
+def test_odd_scale_rows_at_the_end_of_their_memory(cuda_device, op, rows):
+    """Rows of 33 scales, whose last word is the array's in part, with NaN after
+    it and before it."""
+    K, H = (1408, 1056) if op == "dgrad" else (1056, 1408)
+    call, want, size, n, _, (a, sa, w, sw, ro) = _rows_case(op, rows, K, H, 19)
+    flat = torch.full((sa.numel() + 512,), 255, dtype=torch.uint8, device="cuda")
+    inside = flat[256:256 + sa.numel()].view(sa.shape)
+    inside.copy_(sa)
+    if op == "gemm4":
+        out, _ = mg.grouped_mxfp4_gemm(mg.MXFP4(a, inside), mg.MXFP4(w, sw), ro)
+    elif op == "gemm":
+        out, _ = mg.grouped_mxfp8_gemm(mg.MXFP8(a, None, inside, None),
+                                       mg.MXFP8(w, None, sw, None), ro)
+    else:
+        out, _ = mg.grouped_mxfp8_dgrad(mg.MXFP8(a, None, inside, None),
+                                        mg.MXFP8(None, w, None, sw), ro)
+    _check(out, want, size, n, (op, rows))
+
+
 def test_results_repeat(cuda_device):
     """The same call gives the same bits."""
     call, *_ = _rows_case("dgrad", [700, 0, 1300, 130], 1056, 2592, 11)
