@@ -504,8 +504,8 @@ moeact_status mxfp4_dequantize(const void* codes, const void* scales, int32_t sc
  *   out       bf16 or fp32 (out_dtype), rows at a stride of ldo >= the width,
  *             a multiple of 16 bytes; columns past the width are not touched.
  *             wgrad: dw [E, H, K] contiguous; groups without rows get zeros;
- *             accumulate = 1 (fp32 only) adds to what dw holds (rounded to
- *             nearest; the memory's adders take subnormals as zero).
+ *             accumulate = 1 (fp32 only) adds to what dw holds, rounded to
+ *             nearest, subnormals kept.
  *   status    int32 (device): MOEACT_DEV_OK, or MOEACT_DEV_BAD_OFFSETS /
  *             MOEACT_DEV_UNALIGNED_GROUPS, in which case nothing is written.
  * Every pointer 16-byte aligned (offsets 8, status and noop_flag 4), else

@@ -773,7 +773,7 @@ __device__ void gemm_mma(const GroupedGemmParams& p, const GemmSmem& m, uint32_t
 // which clips rows and columns past the output's and leaves the warp free; a
 // product's pieces with fewer rows by plain stores of whole row segments.
 // `add` (fp32): to what the output holds, by a bulk tensor addition in the
-// memory's own units (accumulating wgrad of 128 groups of 512 rows, 2048 x
+// memory's own units, which gives the bits of the warps' additions (accumulating wgrad of 128 groups of 512 rows, 2048 x
 // 1536: 682 us, floor 528; loads, adds and plain stores by the warps: 1,050).
 template <bool WGRAD, bool OUT32>
 __device__ __forceinline__ void store_piece(const GroupedGemmParams& p, const void* tm_out,

@@ -203,7 +203,7 @@ __device__ __forceinline__ void prefetch_map(const void* tmap) {
 }
 
 // Bulk tensor stores from shared memory and (add_*: fp32, rounded to nearest,
-// subnormals as zero) additions to what the output holds; bulk_wait_read: the
+// subnormals kept: held to by the tests) additions to what the output holds; bulk_wait_read: the
 // ones committed have read their shared memory, bulk_wait: they are done.
 __device__ __forceinline__ void store_2d(const void* tmap, const void* src, int x, int y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];"

@@ -798,8 +798,7 @@ def grouped_mxfp8_wgrad(dy, x, row_offs, colblk_offs, *, out_dtype=torch.float32
     """The gradient of grouped_mxfp8_gemm by the weights: dW_e = dY_e^T X_e,
     with dy [M, H] and x [M, K] colwise MXFP8 (grouped calls with these
     offsets).  Returns (dw [E, H, K], status); experts without rows get zeros.
-    accumulate: add to `out` (fp32) instead of overwriting it (subnormals count
-    as zero)."""
+    accumulate: add to `out` (fp32) instead of overwriting it."""
     if dy.col_codes is None or x.col_codes is None or dy.col_scales is None or x.col_scales is None:
         raise ValueError("colwise codes and scales of dy and x are required")
     cy, cx = dy.col_codes, x.col_codes

@@ -160,6 +160,26 @@ def test_wgrad_accumulates(cuda_device):
     assert torch.equal(out, held + once)         # one fp32 addition
 
 
+def test_wgrad_accumulates_subnormals(cuda_device):
+    """What dw holds and what is added, from 2^-100 down to below the smallest
+    number: the bits of one fp32 addition."""
+    g, H, K = _gen(43), 96, 288
+    dy, x = _codes(g, 40, H), _codes(g, 40, K)
+    e = 60 - torch.arange(K, device="cuda", dtype=torch.int32) % 61
+    sx = e.to(torch.uint8).expand(2, K).contiguous()
+    sy = torch.full((2, H), 87, dtype=torch.uint8, device="cuda")
+    a, b = mg.MXFP8(None, dy, None, sy), mg.MXFP8(None, x, None, sx)
+    ro, cb = _dev([0, 40]), _dev([0, 2])
+    once, _ = mg.grouped_mxfp8_wgrad(a, b, ro, cb)
+    held = torch.ldexp(torch.randn(once.shape, generator=g, device="cuda"),
+                       torch.randint(-150, -100, once.shape, generator=g, device="cuda"))
+    small = lambda t: bool(((t != 0) & (t.abs() < 2.0 ** -126)).any())
+    assert small(once) and small(held) and small(held + once)
+    out = held.clone()
+    mg.grouped_mxfp8_wgrad(a, b, ro, cb, out=out, accumulate=True)
+    assert torch.equal(out, held + once)
+
+
 def test_wgrad_accumulates_long_sums(cuda_device):
     splits, H, K = [8193, 0, 20011, 31, 8192, 9000], 1312, 288
     dy, x, sy, sx, ro, cb, want, size = _wgrad_case(splits, H, K, 42)
@@ -222,6 +242,45 @@ def test_long_sums_keep_small_terms(cuda_device, op, rows, cols):
     want = 2.0 ** 23 + (nb - 2) / 32 + last / 1024
     err = (out.double() - want).abs().max().item()
     assert err <= (17.5 if op == "gemm4" else 11.5), err
+
+
+@pytest.mark.parametrize("op", ["gemm", "dgrad", "gemm4"])
+def test_parts_of_sums_add_alike_in_every_row(cuda_device, op):
+    """fp32 sums made in parts, down to parts and results below 2^-126: a row's
+    bits do not depend on how many rows its group has after it.  All rows are
+    alike and so are all groups' weights, whose scales run from 2^-8 to 2^-111
+    over the columns.  The usual tolerance holds where the sum of magnitudes is
+    2^-90 or more: it is 2^-99 there, far above any loss at the 2^-126 where
+    fp32 has fewer bits."""
+    splits, N, n = [64 + 5, 3, 32], 416, 32768 if op == "gemm4" else 16384
+    g, E, M = _gen(50), 3, 104
+    ro = _dev(_offs(splits))
+    wexp = (119 - torch.arange(N, device="cuda") // 4).to(torch.uint8)   # of each output column
+    sa = torch.full((M, n // 32), 40, dtype=torch.uint8, device="cuda")
+    f32 = dict(out_dtype=torch.float32)
+    if op == "gemm4":
+        a, w = _bytes(g, 1, n // 2).expand(M, -1).contiguous(), _bytes(g, N, n // 2).repeat(E, 1)
+        sw = wexp.repeat(E)[:, None].expand(-1, n // 32).contiguous()
+        out, _ = mg.grouped_mxfp4_gemm(mg.MXFP4(a, sa), mg.MXFP4(w, sw), ro, **f32)
+        av, wv = ref.values4(a[:1], sa[:1]), ref.values4(w[:N], sw[:N]).T
+    elif op == "gemm":
+        a, w = _codes(g, 1, n).expand(M, -1).contiguous(), _codes(g, N, n).repeat(E, 1)
+        sw = wexp.repeat(E)[:, None].expand(-1, n // 32).contiguous()
+        out, _ = mg.grouped_mxfp8_gemm(mg.MXFP8(a, None, sa, None), mg.MXFP8(w, None, sw, None),
+                                       ro, **f32)
+        av, wv = ref.values8(a[:1], sa[:1], 1), ref.values8(w[:N], sw[:N], 1).T
+    else:
+        a, w = _codes(g, 1, n).expand(M, -1).contiguous(), _codes(g, n, N).repeat(E, 1)
+        sw = wexp[None].expand(E * n // 32, -1).contiguous()
+        out, _ = mg.grouped_mxfp8_dgrad(mg.MXFP8(a, None, sa, None), mg.MXFP8(None, w, None, sw),
+                                        ro, **f32)
+        av, wv = ref.values8(a[:1], sa[:1], 1), ref.values8(w[:n], sw[:n // 32], 0)
+    bits = out.view(torch.int32)
+    assert torch.equal(bits, bits[:1].expand_as(bits))
+    want, size = av @ wv, av.abs() @ wv.abs()
+    big = size[0] >= 2.0 ** -90
+    assert 0 < int(big.sum()) < N and bool((out[:, -1] == 0).all())
+    _check(out[:1, big], want[:, big], size[:, big], n, op)
 
 
 @pytest.mark.parametrize("splits", [[128, 0, 256], [1280, 128, 640]])
