@@ -482,10 +482,11 @@ moeact_status mxfp4_dequantize(const void* codes, const void* scales, int32_t sc
  *   grouped_mxfp8_dgrad  dx[i, k]  = sum_h dY[i, h] W_e[h, k]
  *   grouped_mxfp8_wgrad  dW_e[h, k] = sum_i dY[i, h] X[i, k]  (i over group e)
  * for row i of group e, of the values the codes and scales stand for.
- * Products are summed in fp32 by the tensor cores (order not specified); the
- * sum is rounded once to the output type.  For fp32 outputs sums of more than
- * 256 steps (of 32 products, MXFP4 64) are made in parts, which are added in
- * fp32.  A NaN scale or code makes the outputs it enters NaN.
+ * Products are summed in fp32 by the tensor cores (order not specified), which
+ * drop what falls below the sum's last bit; the sum is rounded once to the
+ * output type.  Sums of more than 256 steps (of 32 products, MXFP4 64) for fp32
+ * outputs, of more than 16,384 for bf16 ones, are made in parts of 256, which
+ * are added in fp32 (for fp32 outputs in the output itself).  A NaN scale or code makes the outputs it enters NaN.
  *   A, dY (gemm, dgrad)  rowwise codes [M, K] (dgrad [M, H]; MXFP4: [M, K/2]
  *             bytes) and scales [M, K/32] ([M, H/32]) in their scale layout.
  *   W (gemm)  rowwise codes and scales of the dense [E * H, K] matrix.

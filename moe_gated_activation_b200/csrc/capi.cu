@@ -801,8 +801,8 @@ moeact_status check_gemm_common(int64_t M, const int64_t* ro, int32_t E, int32_t
 // 47.7; one group of 1024 rows (128 small tiles) 13.9 and 12.2, of 2048 (256)
 // 14.8 and 17.8; wgrad of 8 x 512 x 512 (128) 9.0 and 7.5, of 64 x 256 x 256
 // (256) 9.4 and 9.8.
-bool gemm_pair(int64_t rows_per_group, int64_t small_tiles, int dev) {
-  return rows_per_group > 128 && small_tiles > g_sms[dev];
+GemmForm gemm_form(int64_t rows_per_group, int64_t small_tiles, int dev) {
+  return rows_per_group > 128 && small_tiles > g_sms[dev] ? kGemmPair : kGemmSingle;
 }
 
 // Forward and dgrad: rows of A [M, K] times each group's W, rows of K
@@ -856,10 +856,11 @@ moeact_status gemm_rows(int op, const void* a_codes, const void* a_scales, int32
   p.status = status;
   p.noop = noop;
   p.err = g_err_ptr[dev];
-  const bool pair = gemm_pair(M / E, std::max<int64_t>(ceil_div(M, 128), std::min<int64_t>(E, M)) *
-                                         ceil_div(N, 128), dev);
+  GemmForm form = gemm_form(
+      M / E, std::max<int64_t>(ceil_div(M, 128), std::min<int64_t>(E, M)) * ceil_div(N, 128), dev);
+  if (!p.out32 && ceil_div(K, op == kGemmFwd4 ? 64 : 32) > kGemmLongSum) form = kGemmLong;
   const int64_t row_bytes = op == kGemmFwd4 ? K / 2 : K;
-  const int box = pair ? kGemmBoxRows : kGemmShortBoxRows;
+  const int box = form == kGemmPair ? kGemmBoxRows : kGemmShortBoxRows;
   GemmMaps tm{};
   if ((st = make_code_map(&tm.a, a_codes, row_bytes, M, box))) return st;
   if (dgrad) st = make_code_map(&tm.b, w_codes, N, wrows, kGemmShortBoxRows);
@@ -875,7 +876,7 @@ moeact_status gemm_rows(int op, const void* a_codes, const void* a_scales, int32
     if (st) return st;
   }
   if ((st = make_out_map(&tm.out, out, p.out32, N, M, ldo, 0))) return st;
-  const cudaError_t e = grouped_gemm_launch(op, pair, p, tm, g_sms[dev], cs);
+  const cudaError_t e = grouped_gemm_launch(op, form, p, tm, g_sms[dev], cs);
   if (e != cudaSuccess) return cuda_fail(e, "grouped product launch");
   return MOEACT_OK;
 }
@@ -890,13 +891,13 @@ cudaError_t grouped_gemm_prepare() {
   return e;
 }
 
-cudaError_t grouped_gemm_launch(int op, bool pair, const GroupedGemmParams& p, const GemmMaps& tm,
+cudaError_t grouped_gemm_launch(int op, GemmForm form, const GroupedGemmParams& p, const GemmMaps& tm,
                                 int n_sms, cudaStream_t stream) {
   switch (op) {
-    case kGemmFwd: return grouped_gemm_launch_fwd(pair, p, tm, n_sms, stream);
-    case kGemmDgrad: return grouped_gemm_launch_dgrad(pair, p, tm, n_sms, stream);
-    case kGemmWgrad: return grouped_gemm_launch_wgrad(pair, p, tm, n_sms, stream);
-    default: return grouped_gemm_launch_fwd4(pair, p, tm, n_sms, stream);
+    case kGemmFwd: return grouped_gemm_launch_fwd(form, p, tm, n_sms, stream);
+    case kGemmDgrad: return grouped_gemm_launch_dgrad(form, p, tm, n_sms, stream);
+    case kGemmWgrad: return grouped_gemm_launch_wgrad(form, p, tm, n_sms, stream);
+    default: return grouped_gemm_launch_fwd4(form, p, tm, n_sms, stream);
   }
 }
 
@@ -1299,9 +1300,12 @@ moeact_status grouped_mxfp8_wgrad(const void* dy_codes, const void* dy_scales,
       if ((st = make_byte_map(&tm.sb, x_scales, K, rows, 128, 32))) return st;
     }
   }
-  const bool pair = gemm_pair(H, num_groups * ceil_div(H, 128) * ceil_div(K, 128), dev);
+  const GemmForm form = gemm_form(H, num_groups * ceil_div(H, 128) * ceil_div(K, 128), dev);
   if ((st = make_out_map(&tm.out, dw, p.out32, K, H, K, num_groups))) return st;
-  const cudaError_t e = grouped_gemm_launch(kGemmWgrad, pair, p, tm, g_sms[dev], cs);
+  cudaError_t e = grouped_gemm_launch(kGemmWgrad, form, p, tm, g_sms[dev], cs);
+  // a group may have a long sum: the first launch leaves those out
+  if (e == cudaSuccess && !p.out32 && ceil_div(M, 32) > kGemmLongSum)
+    e = grouped_gemm_launch(kGemmWgrad, kGemmLong, p, tm, g_sms[dev], cs);
   if (e != cudaSuccess) return cuda_fail(e, "grouped product launch");
   return MOEACT_OK;
 }

@@ -18,6 +18,11 @@ namespace moeact {
 
 enum GemmOp : int { kGemmFwd = 0, kGemmDgrad = 1, kGemmWgrad = 2, kGemmFwd4 = 3 };
 
+// The kernels of an operator: 128 x 128 tiles on single SMs; 256 x 256 tiles on SM
+// pairs; single SMs with room in tensor memory for the running totals of bf16 sums
+// of more than kGemmLongSum steps (and no others).
+enum GemmForm : int { kGemmSingle = 0, kGemmPair = 1, kGemmLong = 2 };
+
 struct GroupedGemmParams {
   const int64_t* row_offs;    // [E + 1]
   const int64_t* cb_offs;     // [E + 1], wgrad only: first block row of each group's scales
@@ -48,6 +53,11 @@ constexpr int kGemmBoxRows = 128, kGemmShortBoxRows = 32;
 // of the [E, R, N] gradients.
 constexpr int kGemmOutRows = 32, kGemmOutBytes = 128;
 
+// Steps (of 32 products, E2M1 64) of a bf16 output's sum that may go through one
+// accumulator, which drops up to 2^-23 of the sum at each: 2^-9 in all, half of
+// what the rounding to bf16 may take.
+constexpr int kGemmLongSum = 16384;
+
 // Row-major scales: 32 bytes (8 words) of 128 rows (A of the one-SM kernels:
 // of 32), or with the blocks outermost 32 rows of 128 columns.
 constexpr int kGemmScaleBytes = 32;
@@ -60,14 +70,13 @@ struct GemmMaps {
 
 // Sets the kernels' shared-memory limits (once per device).
 cudaError_t grouped_gemm_prepare();
-// pair: 256 x 256 tiles on SM pairs, else 128 x 128 tiles on single SMs.
-cudaError_t grouped_gemm_launch(int op, bool pair, const GroupedGemmParams& p, const GemmMaps& tm,
+cudaError_t grouped_gemm_launch(int op, GemmForm form, const GroupedGemmParams& p, const GemmMaps& tm,
                                 int n_sms, cudaStream_t stream);
 
 // One translation unit per operator.
 #define MOEACT_GEMM_UNIT(name)                                                              \
   cudaError_t grouped_gemm_prepare_##name();                                                \
-  cudaError_t grouped_gemm_launch_##name(bool pair, const GroupedGemmParams& p,             \
+  cudaError_t grouped_gemm_launch_##name(GemmForm form, const GroupedGemmParams& p,         \
                                          const GemmMaps& tm, int n_sms, cudaStream_t stream);
 MOEACT_GEMM_UNIT(fwd)
 MOEACT_GEMM_UNIT(dgrad)

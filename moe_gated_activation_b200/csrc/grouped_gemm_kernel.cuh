@@ -58,11 +58,16 @@ constexpr int group_bytes_gemm(int E) { return (E + 1) * (E <= kGroupsInSmem ? 8
 // sum in segments of this many steps, which the epilogue adds with rounding
 // (at most 6.7e-7 there; shorter sums keep their time, one group of 65,536
 // rows, 2048 x 1536, takes 230 us for 215).  bf16 ones, whose own rounding is
-// 2^-8, take one sum.  A multiple of a stage's 4 steps.
+// 2^-8, take one sum of up to kGemmLongSum steps, and longer ones in segments too
+// (kGemmLong; wgrad's by a second launch, which leaves the short groups to the
+// first: on single SMs 2^20 rows on 128 experts, 2048 x 1536, took 3,680 us for
+// 2,380).  A multiple of a stage's 4 steps.
 constexpr int kSegment = 256;
 
-template <int OP, bool PAIR>
+template <int OP, GemmForm FORM>
 struct GemmCfg {
+  static constexpr bool PAIR = FORM == kGemmPair;
+  static constexpr bool kLong = FORM == kGemmLong;
   static constexpr bool kF4 = OP == kGemmFwd4;
   static constexpr bool kWgrad = OP == kGemmWgrad;
   static constexpr bool kAmn = OP == kGemmWgrad;                      // A rows = summed index
@@ -88,6 +93,7 @@ struct GemmCfg {
   static constexpr int kSfCol = 512 - (kStages * kSfPitch + 63) / 64 * 64;
   static constexpr int kAcc1 = PAIR ? kSfCol - kBN : kBN;   // second accumulator's column
   static constexpr int kOverlap = PAIR ? kBN - kAcc1 : 0;
+  static constexpr int kTotal = 2 * kBN;   // kLong: the running totals
   static constexpr int kABox = kAmn || !PAIR ? kGemmShortBoxRows : kGemmBoxRows;
   static constexpr int kBBox = kBmn ? kGemmShortBoxRows : kGemmBoxRows;
   static constexpr int kStageBytes = 2 * kTileBytes;
@@ -100,6 +106,7 @@ struct GemmCfg {
                     kFixed + 1024 + group_bytes_gemm(kGroupsInSmem) <= 232448,
                 "shared memory of a block");
   static_assert(kAcc1 >= 0 && kAcc1 + kBN <= kSfCol, "tensor-memory columns overlap");
+  static_assert(!kLong || kTotal + kBN <= kSfCol, "tensor-memory columns overlap");
   static_assert(kOverlap % 64 == 0, "the overlap is drained in chunks of 64 columns");
 };
 
@@ -181,6 +188,9 @@ struct GemmWalk {
       r.k0 = row_off(p, m, e);
       r.krows = row_off(p, m, e + 1) - (int)r.k0;
       r.kb = (r.krows + 31) >> 5;
+      // long bf16 sums are the kLong kernel's: nothing to do here, or only these
+      if (C::kLong ? r.kb <= kGemmLongSum : !p.out32 && r.kb > kGemmLongSum)
+        r.kb = r.krows = r.rows = 0;
     } else {
       int hi = p.E - 1;   // largest e with pre[e] <= mt (then mt < pre[e + 1])
       while (e < hi) {
@@ -699,6 +709,12 @@ __device__ void gemm_producer(const GroupedGemmParams& p, const GemmSmem& m, con
   __syncwarp();
 }
 
+// Steps of a sum of `mmas` that one accumulator takes.
+template <typename C>
+__device__ __forceinline__ int segment_steps(const GroupedGemmParams& p, int mmas) {
+  return C::kLong || p.out32 ? kSegment : mmas;
+}
+
 // ------------------------------------------------------------ MMAs
 // Warp 9 of the (first) SM, converged, one elected lane issuing, so that the
 // descriptors are warp-uniform.
@@ -722,7 +738,7 @@ __device__ void gemm_mma(const GroupedGemmParams& p, const GemmSmem& m, uint32_t
     const int kb = C::kWgrad ? walk.tile(p, m, 0).kb : p.K >> 5;
     if (kb == 0) continue;
     const int mmas = (kb * 32 + C::kMmaK - 1) / C::kMmaK;
-    const int segment = p.out32 ? kSegment : mmas;
+    const int segment = segment_steps<C>(p, mmas);
     for (int i1 = 0; i1 < mmas; i1 += segment, ++n) {
       // the tile (or segment) whose columns this one takes: the last but one,
       // or with overlapping accumulators the last
@@ -773,8 +789,9 @@ __device__ void gemm_mma(const GroupedGemmParams& p, const GemmSmem& m, uint32_t
 // which clips rows and columns past the output's and leaves the warp free; a
 // product's pieces with fewer rows by plain stores of whole row segments.
 // `add` (fp32): to what the output holds, by a bulk tensor addition in the
-// memory's own units, which gives the bits of the warps' additions (accumulating wgrad of 128 groups of 512 rows, 2048 x
-// 1536: 682 us, floor 528; loads, adds and plain stores by the warps: 1,050).
+// memory's own units, which gives the bits of the warps' additions
+// (accumulating wgrad of 128 groups of 512 rows, 2048 x 1536: 682 us, floor
+// 528; loads, adds and plain stores by the warps: 1,050).
 template <bool WGRAD, bool OUT32>
 __device__ __forceinline__ void store_piece(const GroupedGemmParams& p, const void* tm_out,
                                             unsigned char* stg, const uint4* v,
@@ -838,6 +855,60 @@ __device__ __forceinline__ void store_piece(const GroupedGemmParams& p, const vo
   __syncwarp();
 }
 
+// A tile whose bf16 sums are in segments: adds each to the totals in tensor memory
+// and gives the last's, rounded, to put(values, column).  n: the accumulators
+// used so far.  (Kernels of their own have it: in those for short sums it cost
+// every call, gemm4 decode 22.6 -> 24.6 us.)
+template <typename C, typename Put>
+__device__ __forceinline__ bool gemm_long_tile(const GroupedGemmParams& p, const GemmSmem& m,
+                                               uint32_t tbase, int mmas, int& n, const Put& put) {
+  const int q = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const uint32_t quarter = tbase + ((uint32_t)(32 * q) << 16);
+  for (int i = 0; i < mmas; i += kSegment, ++n) {
+    const int b = n & 1;
+    if (!__all_sync(kFull, tc::sleep<C::kOrder>(m.d_full + b, (uint32_t)(n >> 1) & 1u)) ||
+        gemm_aborted(m)) {
+      gemm_abort(p, m);
+      return false;
+    }
+    tc::fence_after();
+    const bool first = i == 0, last = i + kSegment >= mmas;
+#pragma unroll 1
+    for (int c = 0; c < C::kBN; c += 64) {
+      uint4 w[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t v[32], t[32];
+        tc::ld32(quarter + b * C::kAcc1 + c + 32 * h, v);
+        if (!first) tc::ld32(quarter + C::kTotal + c + 32 * h, t);
+        tc::wait_ld();
+        tc::tie(v);
+        if (!first) {
+          tc::tie(t);
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            v[j] = __float_as_uint(__fadd_rn(__uint_as_float(t[j]), __uint_as_float(v[j])));
+        }
+        if (!last) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            tc::st4(quarter + C::kTotal + c + 32 * h + j, v[j], v[j + 1], v[j + 2], v[j + 3]);
+        }
+        uint32_t* x = reinterpret_cast<uint32_t*>(w) + 16 * h;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          x[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+      }
+      tc::wait_st();
+      if (last) put(w, c);
+    }
+    tc::fence_before();
+    __syncwarp();
+    if (lane == 0) tc::arrive_leader<C::kOrder>(tc::leader_addr(m.d_empty) + 8 * b);
+  }
+  return true;
+}
+
 template <typename C>
 __device__ void gemm_epilogue(const GroupedGemmParams& p, const GemmSmem& m, const void* tm_out,
                               uint32_t tbase, int tiles, int first, int step, int rank,
@@ -874,7 +945,12 @@ __device__ void gemm_epilogue(const GroupedGemmParams& p, const GemmSmem& m, con
       }
       continue;
     }
-    for (int seg = 0; seg < segments; ++seg, ++n, add = true) {
+    if constexpr (C::kLong) {
+      if (!gemm_long_tile<C>(p, m, tbase, mmas, n, [&](const uint4* w, int c) {
+            if (tile.n0 + c < p.N && rows > 0) put(Bf16(), w, tile.n0 + c);
+          }))
+        return;
+    } else for (int seg = 0; seg < segments; ++seg, ++n, add = true) {
       if (seg && lane == 0) tc::bulk_wait();   // the stores that it adds to are done
       const int b = n & 1;
       if (!__all_sync(kFull, tc::sleep<C::kOrder>(m.d_full + b, (uint32_t)(n >> 1) & 1u)) || gemm_aborted(m)) {
@@ -939,14 +1015,15 @@ __device__ void gemm_epilogue(const GroupedGemmParams& p, const GemmSmem& m, con
 }
 
 // ------------------------------------------------------------ kernel
-template <int OP, bool PAIR>
-__global__ void __launch_bounds__(GemmCfg<OP, PAIR>::kThreads, 1)
+template <int OP, GemmForm FORM>
+__global__ void __launch_bounds__(GemmCfg<OP, FORM>::kThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
                         const __grid_constant__ CUtensorMap tm_b,
                         const __grid_constant__ CUtensorMap tm_sa,
                         const __grid_constant__ CUtensorMap tm_sb,
                         const __grid_constant__ CUtensorMap tm_out, const GroupedGemmParams p) {
-  using C = GemmCfg<OP, PAIR>;
+  using C = GemmCfg<OP, FORM>;
+  constexpr bool PAIR = C::PAIR;
   if (p.noop != nullptr && *p.noop != 0) return;
   extern __shared__ __align__(1024) unsigned char gemm_smem[];
   unsigned char* base = gemm_smem + ((1024u - (smem_addr(gemm_smem) & 1023u)) & 1023u);
@@ -1078,24 +1155,24 @@ __global__ void __launch_bounds__(GemmCfg<OP, PAIR>::kThreads, 1)
   }
 }
 
-template <int OP, bool PAIR>
+template <int OP, GemmForm FORM>
 int gemm_smem_bytes(int E) {
-  using C = GemmCfg<OP, PAIR>;
+  using C = GemmCfg<OP, FORM>;
   return 1024 + C::kFixed + group_bytes_gemm(E);
 }
 
-template <int OP, bool PAIR>
+template <int OP, GemmForm FORM>
 cudaError_t gemm_prepare_one(int max_groups) {
-  return cudaFuncSetAttribute(grouped_gemm_kernel<OP, PAIR>,
+  return cudaFuncSetAttribute(grouped_gemm_kernel<OP, FORM>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              std::max(gemm_smem_bytes<OP, PAIR>(max_groups),
-                                       gemm_smem_bytes<OP, PAIR>(kGroupsInSmem)));
+                              std::max(gemm_smem_bytes<OP, FORM>(max_groups),
+                                       gemm_smem_bytes<OP, FORM>(kGroupsInSmem)));
 }
 
-template <int OP, bool PAIR>
+template <int OP, GemmForm FORM>
 cudaError_t gemm_launch_one(const GroupedGemmParams& p, const GemmMaps& tm, int n_sms,
                             cudaStream_t stream) {
-  using C = GemmCfg<OP, PAIR>;
+  using C = GemmCfg<OP, FORM>;
   // at most as many row tiles as full ones and one more per group
   const int64_t row_tiles = C::kWgrad ? (int64_t)p.E * ((p.R + C::kTM - 1) / C::kTM)
                                       : p.M / C::kTM + (p.E < p.M ? p.E : p.M);
@@ -1104,7 +1181,7 @@ cudaError_t gemm_launch_one(const GroupedGemmParams& p, const GemmMaps& tm, int 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * C::kCG));
   cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = gemm_smem_bytes<OP, PAIR>(p.E);
+  cfg.dynamicSmemBytes = gemm_smem_bytes<OP, FORM>(p.E);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -1112,7 +1189,7 @@ cudaError_t gemm_launch_one(const GroupedGemmParams& p, const GemmMaps& tm, int 
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, grouped_gemm_kernel<OP, PAIR>, tm.a, tm.b, tm.sa, tm.sb, tm.out,
+  return cudaLaunchKernelEx(&cfg, grouped_gemm_kernel<OP, FORM>, tm.a, tm.b, tm.sa, tm.sb, tm.out,
                             p);
 }
 
@@ -1123,12 +1200,14 @@ cudaError_t gemm_launch_one(const GroupedGemmParams& p, const GemmMaps& tm, int 
 #define MOEACT_DEFINE_GEMM_UNIT(name, OP)                                                       \
   namespace moeact {                                                                            \
   cudaError_t grouped_gemm_prepare_##name() {                                                   \
-    cudaError_t e = gemm_prepare_one<OP, false>(MOEACT_MAX_GROUPS);                             \
-    return e != cudaSuccess ? e : gemm_prepare_one<OP, true>(MOEACT_MAX_GROUPS);                \
+    cudaError_t e = gemm_prepare_one<OP, kGemmSingle>(MOEACT_MAX_GROUPS);                       \
+    if (e == cudaSuccess) e = gemm_prepare_one<OP, kGemmPair>(MOEACT_MAX_GROUPS);               \
+    return e != cudaSuccess ? e : gemm_prepare_one<OP, kGemmLong>(MOEACT_MAX_GROUPS);           \
   }                                                                                             \
-  cudaError_t grouped_gemm_launch_##name(bool pair, const GroupedGemmParams& p,                 \
+  cudaError_t grouped_gemm_launch_##name(GemmForm form, const GroupedGemmParams& p,             \
                                          const GemmMaps& tm, int n_sms, cudaStream_t stream) {  \
-    return pair ? gemm_launch_one<OP, true>(p, tm, n_sms, stream)                               \
-                : gemm_launch_one<OP, false>(p, tm, n_sms, stream);                             \
+    return form == kGemmPair   ? gemm_launch_one<OP, kGemmPair>(p, tm, n_sms, stream)           \
+           : form == kGemmLong ? gemm_launch_one<OP, kGemmLong>(p, tm, n_sms, stream)           \
+                               : gemm_launch_one<OP, kGemmSingle>(p, tm, n_sms, stream);        \
   }                                                                                             \
   }

@@ -244,6 +244,76 @@ def test_long_sums_keep_small_terms(cuda_device, op, rows, cols):
     assert err <= (17.5 if op == "gemm4" else 11.5), err
 
 
+@pytest.mark.parametrize("op", ["wgrad", "gemm", "dgrad", "gemm4"])
+def test_long_bf16_sums_keep_small_terms(cuda_device, op):
+    """A bf16 output's sum of 131,072 steps, the first of 2^23 and the others of
+    1/2, which one accumulator drops: 2^16 in all, a whole step of bf16 there.
+    In parts of 256 steps only the first part's are dropped, less than 128; the
+    other parts are exact, and so are their additions, of integers below 2^24.
+    The rounding takes half a step, 2^15, at most."""
+    per, steps = (64, 131072) if op == "gemm4" else (32, 131072)
+    n, m, cols = per * steps, 32, 64
+    ones8 = lambda *s: torch.full(s, 0x38, dtype=torch.uint8, device="cuda")
+    ones4 = lambda *s: torch.full(s, 0x22, dtype=torch.uint8, device="cuda")
+    scale = lambda *s: torch.full(s, 127, dtype=torch.uint8, device="cuda")
+    exps = torch.full((n // 32,), 127 - (7 if op == "gemm4" else 6), dtype=torch.uint8, device="cuda")
+    exps[0] = 127 + 18
+    if op == "gemm4":
+        exps[1] = 0      # the first step's other half
+    byrow, ro = exps.expand(m, -1).contiguous(), _dev([0, m])
+    if op == "wgrad":
+        dy = mg.MXFP8(None, ones8(n, m), None, exps[:, None].expand(-1, m).contiguous())
+        x = mg.MXFP8(None, ones8(n, cols), None, scale(n // 32, cols))
+        out, st = mg.grouped_mxfp8_wgrad(dy, x, _dev([0, n]), _dev([0, n // 32]),
+                                         out_dtype=torch.bfloat16)
+    elif op == "gemm":
+        out, st = mg.grouped_mxfp8_gemm(mg.MXFP8(ones8(m, n), None, byrow, None),
+                                        mg.MXFP8(ones8(cols, n), None, scale(cols, n // 32), None), ro)
+    elif op == "dgrad":
+        out, st = mg.grouped_mxfp8_dgrad(mg.MXFP8(ones8(m, n), None, byrow, None),
+                                         mg.MXFP8(None, ones8(n, cols), None, scale(n // 32, cols)), ro)
+    else:
+        out, st = mg.grouped_mxfp4_gemm(mg.MXFP4(ones4(m, n // 2), byrow),
+                                        mg.MXFP4(ones4(cols, n // 2), scale(cols, n // 32)), ro)
+    assert int(st) == 0 and out.dtype == torch.bfloat16
+    want = 2.0 ** 23 + (steps - 1) / 2
+    err = (out.double() - want).abs().max().item()
+    assert err <= 2.0 ** 15 + 128, err
+
+
+@pytest.mark.parametrize("op", ["wgrad", "gemm", "dgrad", "gemm4"])
+def test_long_bf16_sums_are_the_fp32_ones_rounded(cuda_device, op):
+    """Both are made of the same parts, added in the same order; several such
+    tiles and short ones follow one another on an SM."""
+    g = _gen(51)
+    n = (1 << 20) + 32 if op == "gemm4" else (1 << 19) + 32      # 16385 steps
+    if op == "gemm4":
+        n += 32
+    if op == "wgrad":
+        splits, H, K = [n, 0, 8000, 600001, 77, 31] + [5] * 20, 288, 1312
+        M, offs, cb = sum(splits), _offs(splits), _blocks(splits)
+        dy = mg.MXFP8(None, _codes(g, M, H), None, _scales(g, cb[-1], H))
+        x = mg.MXFP8(None, _codes(g, M, K), None, _scales(g, cb[-1], K))
+        call = lambda dt: mg.grouped_mxfp8_wgrad(dy, x, _dev(offs), _dev(cb), out_dtype=dt)
+    else:
+        M, N, ro = 1030, 2592, _dev([0, 1030])
+        if op == "gemm4":
+            a = mg.MXFP4(_bytes(g, M, n // 2), _scales(g, M, n // 32))
+            w = mg.MXFP4(_bytes(g, N, n // 2), _scales(g, N, n // 32))
+            call = lambda dt: mg.grouped_mxfp4_gemm(a, w, ro, out_dtype=dt)
+        else:
+            a = mg.MXFP8(_codes(g, M, n), None, _scales(g, M, n // 32), None)
+            if op == "gemm":
+                w = mg.MXFP8(_codes(g, N, n), None, _scales(g, N, n // 32), None)
+                call = lambda dt: mg.grouped_mxfp8_gemm(a, w, ro, out_dtype=dt)
+            else:
+                w = mg.MXFP8(None, _codes(g, n, N), None, _scales(g, n // 32, N))
+                call = lambda dt: mg.grouped_mxfp8_dgrad(a, w, ro, out_dtype=dt)
+    short, st = call(torch.bfloat16)
+    full, _ = call(torch.float32)
+    assert int(st) == 0 and torch.equal(short, full.bfloat16())
+
+
 @pytest.mark.parametrize("op", ["gemm", "dgrad", "gemm4"])
 def test_parts_of_sums_add_alike_in_every_row(cuda_device, op):
     """fp32 sums made in parts, down to parts and results below 2^-126: a row's
