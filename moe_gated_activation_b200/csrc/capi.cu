@@ -341,24 +341,6 @@ moeact_status make_code_map(CUtensorMap* map, const void* base, int64_t bytes, i
   return MOEACT_OK;
 }
 
-// wgrad's map of a code matrix of `rows` rows of `bytes` bytes: [rows][32][bytes],
-// for each row that row and the 31 after it, in boxes of 32 rows of 128 bytes,
-// swizzled as above.  A box at (x, y, z) with y in (-32, 0] holds -y rows of
-// zeros, then rows z .. z + 31 + y (the last of them below `rows`: the caller's
-// part).
-moeact_status make_block_map(CUtensorMap* map, const void* base, int64_t bytes, int64_t rows) {
-  const cuuint64_t dims[3] = {(cuuint64_t)bytes, 32, (cuuint64_t)rows};
-  const cuuint64_t strides[2] = {(cuuint64_t)bytes, (cuuint64_t)bytes};
-  const cuuint32_t box[3] = {128, 32, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims,
-                              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(MOEACT_ECUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
-  return MOEACT_OK;
-}
-
 // Tensor map of a byte matrix (contiguous rows of `bytes`, a multiple of 16) in
 // plain boxes.
 moeact_status make_byte_map(CUtensorMap* map, const void* base, int64_t bytes, int64_t rows,
@@ -1292,8 +1274,10 @@ moeact_status grouped_mxfp8_wgrad(const void* dy_codes, const void* dy_scales,
   p.err = g_err_ptr[dev];
   GemmMaps tm{};
   if (M > 0) {
-    if ((st = make_block_map(&tm.a, dy_codes, H, M))) return st;
-    if ((st = make_block_map(&tm.b, x_codes, K, M))) return st;
+    if ((st = make_code_map(&tm.a, dy_codes, H, M, kGemmShortBoxRows))) return st;
+    if ((st = make_code_map(&tm.b, x_codes, K, M, kGemmShortBoxRows))) return st;
+    if ((st = make_code_map(&tm.ra, dy_codes, H, M, 1))) return st;
+    if ((st = make_code_map(&tm.rb, x_codes, K, M, 1))) return st;
     if (!p.a_tiled) {
       const int64_t rows = std::min<int64_t>(scale_rows, ceil_div(M, 32) + num_groups);
       if ((st = make_byte_map(&tm.sa, dy_scales, H, rows, 128, 32))) return st;

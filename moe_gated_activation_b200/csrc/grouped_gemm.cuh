@@ -66,6 +66,7 @@ struct GemmMaps {
   CUtensorMap a, b;     // code matrices
   CUtensorMap sa, sb;   // scales, where row-major with steps of 16 bytes
   CUtensorMap out;
+  CUtensorMap ra, rb;   // wgrad: the code matrices row by row
 };
 
 // Sets the kernels' shared-memory limits (once per device).

@@ -645,15 +645,16 @@ __device__ __forceinline__ void gemm_scales_any(const GroupedGemmParams& p, cons
 // Warp 8.  wgrad: blocks of 32 rows of a group at any row.  The rows past the
 // group's end are the next group's: they must not meet in the sum, and a zero
 // times a NaN of theirs would not be zero, so they are zeros in both operands.
-// The copies put them there: the maps are [rows][32][columns], row z's 32 next
-// rows, and a box that starts `32 - r` rows before them is filled with that many
-// zeros, then the r rows.  (Both operands' rows move alike, so the sum is the
-// same.  A warp that cleared the rows after the copies had to order its stores
-// between the SMs of a pair: a release to the pair in every tile, wgrad train
-// 456 us for 417.)
+// A group's last block is therefore copied row by row, the rows past its end
+// from past the array's, which read as zeros.  (A warp that cleared them after
+// the copies had to release its stores to the other SM of a pair, which takes
+// as long as all that the SM has under way: wgrad short 32.7 us for 28.8, wgrad
+// train 443 for 441.  That block first of a tile's, on its way while the tile
+// before is summed: 429 for 434, short 30 for 29.)
 template <typename C>
 __device__ __forceinline__ void gemm_copy_codes(const GroupedGemmParams& p, const GemmSmem& m,
-                                                const void* tm_a, const void* tm_b, int tiles,
+                                                const void* tm_a, const void* tm_b,
+                                                const void* tm_ra, const void* tm_rb, int tiles,
                                                 int first, int step, int rank) {
   const uint32_t full0 = tc::leader_addr(m.full);
   int slot = 0;
@@ -681,11 +682,17 @@ __device__ __forceinline__ void gemm_copy_codes(const GroupedGemmParams& p, cons
       else
         tc::arrive_tx_leader(bar, bytes);
       if constexpr (C::kWgrad) {
-        for (int i = 0; i < blocks; ++i) {
-          const int row = 32 * (4 * s + i), y = min(0, tile.krows - row - 32);
-          tc::load_3d<C::kCG>(da + i * C::kABox * 128, tm_a, (int)tile.row0, y,
-                              (int)tile.k0 + row, bar);
-          tc::load_3d<C::kCG>(db + i * C::kBBox * 128, tm_b, col_b, y, (int)tile.k0 + row, bar);
+        const int row = (int)tile.k0 + 128 * s, left = tile.krows - 128 * s;
+        for (int i = 0; 32 * (i + 1) <= left && i < 4; ++i) {
+          tc::load_2d<C::kCG>(da + 4096 * i, tm_a, (int)tile.row0, row + 32 * i, bar);
+          tc::load_2d<C::kCG>(db + 4096 * i, tm_b, col_b, row + 32 * i, bar);
+        }
+        if (left < 128 && (left & 31) != 0) {
+          for (int j = left & ~31; j < ((left + 31) & ~31); ++j) {
+            const int y = j < left ? row + j : (int)p.M;
+            tc::load_2d<C::kCG>(da + 128 * j, tm_ra, (int)tile.row0, y, bar);
+            tc::load_2d<C::kCG>(db + 128 * j, tm_rb, col_b, y, bar);
+          }
         }
       } else {
         for (int i = 0; i < na; ++i)
@@ -704,8 +711,10 @@ __device__ __forceinline__ void gemm_copy_codes(const GroupedGemmParams& p, cons
 // 7% of products over short sums.)
 template <typename C>
 __device__ void gemm_producer(const GroupedGemmParams& p, const GemmSmem& m, const void* tm_a,
-                              const void* tm_b, int tiles, int first, int step, int rank) {
-  if (tc::elect_one()) gemm_copy_codes<C>(p, m, tm_a, tm_b, tiles, first, step, rank);
+                              const void* tm_b, const void* tm_ra, const void* tm_rb, int tiles,
+                              int first, int step, int rank) {
+  if (tc::elect_one())
+    gemm_copy_codes<C>(p, m, tm_a, tm_b, tm_ra, tm_rb, tiles, first, step, rank);
   __syncwarp();
 }
 
@@ -1021,7 +1030,9 @@ __global__ void __launch_bounds__(GemmCfg<OP, FORM>::kThreads, 1)
                         const __grid_constant__ CUtensorMap tm_b,
                         const __grid_constant__ CUtensorMap tm_sa,
                         const __grid_constant__ CUtensorMap tm_sb,
-                        const __grid_constant__ CUtensorMap tm_out, const GroupedGemmParams p) {
+                        const __grid_constant__ CUtensorMap tm_out,
+                        const __grid_constant__ CUtensorMap tm_ra,
+                        const __grid_constant__ CUtensorMap tm_rb, const GroupedGemmParams p) {
   using C = GemmCfg<OP, FORM>;
   constexpr bool PAIR = C::PAIR;
   if (p.noop != nullptr && *p.noop != 0) return;
@@ -1049,6 +1060,7 @@ __global__ void __launch_bounds__(GemmCfg<OP, FORM>::kThreads, 1)
     if (p.M > 0) {
       tc::prefetch_map(&tm_a);
       tc::prefetch_map(&tm_b);
+      if (C::kWgrad) tc::prefetch_map(&tm_ra), tc::prefetch_map(&tm_rb);
       if (scales_by_map(scale_mode(C::kAmn, p.a_tiled, p.K >> 5))) tc::prefetch_map(&tm_sa);
       if (scales_by_map(scale_mode(C::kBmn, p.b_tiled, p.K >> 5))) tc::prefetch_map(&tm_sb);
     }
@@ -1134,7 +1146,7 @@ __global__ void __launch_bounds__(GemmCfg<OP, FORM>::kThreads, 1)
   if (warp < 4 || warp >= 12)
     gemm_epilogue<C>(p, m, &tm_out, tbase, tiles, first, step, rank, warp >= 12);
   else if (warp < 8) gemm_scales_any<C>(p, m, tbase, warp - 4);
-  else if (warp == 8) gemm_producer<C>(p, m, &tm_a, &tm_b, tiles, first, step, rank);
+  else if (warp == 8) gemm_producer<C>(p, m, &tm_a, &tm_b, &tm_ra, &tm_rb, tiles, first, step, rank);
   else if (warp == 10) gemm_scale_loader<C>(p, m, &tm_sa, &tm_sb, tiles, first, step, rank);
   else if (warp == 9 && rank == 0) gemm_mma<C>(p, m, tbase, tiles, first, step);
 
@@ -1190,7 +1202,7 @@ cudaError_t gemm_launch_one(const GroupedGemmParams& p, const GemmMaps& tm, int 
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, grouped_gemm_kernel<OP, FORM>, tm.a, tm.b, tm.sa, tm.sb, tm.out,
-                            p);
+                            tm.ra, tm.rb, p);
 }
 
 }  // namespace

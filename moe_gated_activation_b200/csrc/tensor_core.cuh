@@ -162,7 +162,7 @@ __device__ __forceinline__ void arrive_tx_leader(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;"
                ::"r"(bar), "r"(bytes) : "memory");
 }
-// Tile loads into this SM's shared memory, completing on the barrier at
+// 2-D tile load into this SM's shared memory, completing on the barrier at
 // cluster address `bar` (this SM's, or with CG = 2 the pair's first SM's).
 template <int CG>
 __device__ __forceinline__ void load_2d(void* dst, const void* tmap, int x, int y, uint32_t bar) {
@@ -177,24 +177,6 @@ __device__ __forceinline__ void load_2d(void* dst, const void* tmap, int x, int 
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
         "bytes [%0], [%1, {%2, %3}], [%4];"
         ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-template <int CG>
-__device__ __forceinline__ void load_3d(void* dst, const void* tmap, int x, int y, int z,
-                                        uint32_t bar) {
-  if constexpr (CG == 1)
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4}], [%5];"
-        ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z),
-        "r"(bar)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
-        "bytes [%0], [%1, {%2, %3, %4}], [%5];"
-        ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z),
-        "r"(bar)
         : "memory");
 }
 

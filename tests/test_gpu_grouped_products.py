@@ -468,6 +468,37 @@ def test_nan_after_every_group_end(cuda_device, seed):
         _check(dw[::2], want[::2], size[::2], max(splits), splits)
 
 
+@pytest.mark.parametrize("splits", [[5120], [3, 5110, 7], [1, 0, 31, 5087, 1], [5089, 31]])
+def test_wgrad_of_whole_allocations(cuda_device, splits):
+    """Code arrays that fill allocations of whole pages from their first byte to
+    their last: the blocks at either end touch nothing beside them."""
+    H, K = 4096, 6144
+    dy, x, sy, sx, ro, cb, want, size = _wgrad_case(splits, H, K, 21)
+    assert dy.numel() % (2 << 20) == 0 and x.numel() % (2 << 20) == 0
+    for dt in HALF:
+        dw, st = mg.grouped_mxfp8_wgrad(mg.MXFP8(None, dy, None, sy), mg.MXFP8(None, x, None, sx),
+                                        ro, cb, out_dtype=dt)
+        assert int(st) == 0
+        _check(dw, want, size, max(splits), splits)
+
+
+@pytest.mark.parametrize("M,H,K", [(1, 32, 32), (6, 3648, 3008), (9, 96, 4096), (40, 2592, 320)])
+def test_wgrad_of_few_rows(cuda_device, M, H, K):
+    """A few rows on a few groups, in arrays at ever other places."""
+    g = torch.Generator().manual_seed(M)
+    keep = []
+    for i in range(12):
+        cuts = sorted(int(v) for v in torch.randint(0, M + 1, (3,), generator=g))
+        splits = [b - a for a, b in zip([0] + cuts, cuts + [M])]
+        case = _wgrad_case(splits, H, K, 22 + i)
+        dy, x, sy, sx, ro, cb, want, size = case
+        dw, st = mg.grouped_mxfp8_wgrad(mg.MXFP8(None, dy, None, sy), mg.MXFP8(None, x, None, sx),
+                                        ro, cb)
+        assert int(st) == 0
+        _check(dw, want, size, M, splits)
+        keep.append((dy, x))
+
+
 def test_extreme_scales(cuda_device):
     """Scales whose product leaves fp32's range overflow to infinity and
     vanish to zero; 2^-127 times 2^127 is one."""
