@@ -57,7 +57,7 @@ constexpr int group_bytes_gemm(int E) { return (E + 1) * (E <= kGroupsInSmem ? 8
 // rows relative to the norm (6.8e-6 at 62,348).  fp32 outputs therefore take a
 // sum in segments of this many steps, which the epilogue adds with rounding
 // (at most 6.7e-7 there; shorter sums keep their time, one group of 65,536
-// rows, 2048 x 1536, takes 230 us for 215).  bf16 ones, whose own rounding is
+// rows, 2048 x 1536, takes 203 us for 186).  bf16 ones, whose own rounding is
 // 2^-8, take one sum of up to kGemmLongSum steps, and longer ones in segments too
 // (kGemmLong; wgrad's by a second launch, which leaves the short groups to the
 // first: on single SMs 2^20 rows on 128 experts, 2048 x 1536, took 3,680 us for
