@@ -314,6 +314,41 @@ def test_long_bf16_sums_are_the_fp32_ones_rounded(cuda_device, op):
     assert int(st) == 0 and torch.equal(short, full.bfloat16())
 
 
+def test_long_bf16_wgrad_in_a_graph(cuda_device):
+    """Its two launches follow the offsets of each replay, a long group beside an
+    empty or a short one (of at most 256 steps: one sum for fp32 outputs too);
+    bad offsets and a set no-op flag write nothing."""
+    g, M, H, K = _gen(52), (1 << 19) + 8192 + 96, 160, 192
+    nb = M // 32 + 2
+    dy = mg.MXFP8(None, _codes(g, M, H), None, _scales(g, nb, H))
+    x = mg.MXFP8(None, _codes(g, M, K), None, _scales(g, nb, K))
+    ro, cb, st = _dev([0, M, M]), _dev([0, M // 32, M // 32]), torch.zeros(1, dtype=torch.int32, device="cuda")
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.empty(2, H, K, dtype=torch.bfloat16, device="cuda")
+    call = lambda: mg.grouped_mxfp8_wgrad(dy, x, ro, cb, out=out, status=st, noop_flag=flag)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for splits in ([M, 0], [8000, M - 8000], [M - 8187, 8187], [41, M - 41]):
+        ro.copy_(_dev(_offs(splits)))
+        cb.copy_(_dev(_blocks(splits)))
+        full, _ = mg.grouped_mxfp8_wgrad(dy, x, ro, cb)
+        out.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(st) == 0 and torch.equal(out, full.bfloat16()), splits
+    out.fill_(7)
+    flag.fill_(1)
+    graph.replay()
+    flag.fill_(0)
+    ro.copy_(_dev([0, M + 1, M]))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert int(st) == _capi.DEV_BAD_OFFSETS and bool((out == 7).all())
+
+
 @pytest.mark.parametrize("op", ["gemm", "dgrad", "gemm4"])
 def test_parts_of_sums_add_alike_in_every_row(cuda_device, op):
     """fp32 sums made in parts, down to parts and results below 2^-126: a row's
