@@ -486,7 +486,8 @@ moeact_status mxfp4_dequantize(const void* codes, const void* scales, int32_t sc
  * drop what falls below the sum's last bit; the sum is rounded once to the
  * output type.  Sums of more than 256 steps (of 32 products, MXFP4 64) for fp32
  * outputs, of more than 16,384 for bf16 ones, are made in parts of 256, which
- * are added in fp32 (for fp32 outputs in the output itself).  A NaN scale or code makes the outputs it enters NaN.
+ * are added in fp32 (for fp32 outputs in the output itself).  A NaN scale or
+ * code makes the outputs it enters NaN.
  *   A, dY (gemm, dgrad)  rowwise codes [M, K] (dgrad [M, H]; MXFP4: [M, K/2]
  *             bytes) and scales [M, K/32] ([M, H/32]) in their scale layout.
  *   W (gemm)  rowwise codes and scales of the dense [E * H, K] matrix.

@@ -873,8 +873,8 @@ cudaError_t grouped_gemm_prepare() {
   return e;
 }
 
-cudaError_t grouped_gemm_launch(int op, GemmForm form, const GroupedGemmParams& p, const GemmMaps& tm,
-                                int n_sms, cudaStream_t stream) {
+cudaError_t grouped_gemm_launch(int op, GemmForm form, const GroupedGemmParams& p,
+                                const GemmMaps& tm, int n_sms, cudaStream_t stream) {
   switch (op) {
     case kGemmFwd: return grouped_gemm_launch_fwd(form, p, tm, n_sms, stream);
     case kGemmDgrad: return grouped_gemm_launch_dgrad(form, p, tm, n_sms, stream);

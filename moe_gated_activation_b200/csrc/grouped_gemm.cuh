@@ -71,8 +71,8 @@ struct GemmMaps {
 
 // Sets the kernels' shared-memory limits (once per device).
 cudaError_t grouped_gemm_prepare();
-cudaError_t grouped_gemm_launch(int op, GemmForm form, const GroupedGemmParams& p, const GemmMaps& tm,
-                                int n_sms, cudaStream_t stream);
+cudaError_t grouped_gemm_launch(int op, GemmForm form, const GroupedGemmParams& p,
+                                const GemmMaps& tm, int n_sms, cudaStream_t stream);
 
 // One translation unit per operator.
 #define MOEACT_GEMM_UNIT(name)                                                              \

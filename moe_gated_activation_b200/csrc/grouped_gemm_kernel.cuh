@@ -16,7 +16,8 @@
 //   warp 8     TMA loads of the code tiles (128 rows x 128 bytes each);
 //   warp 9     tensor-memory allocation; in the pair's first SM the MMAs;
 //   warp 10    the scales' copies into shared memory, some chunks ahead;
-//   warps 12-15  wgrad on pairs: a second set of epilogue warps.
+//   warps 12-15  wgrad on pairs: a second set of epilogue warps (warp 11 does
+//              nothing: the sets are groups of four).
 // One ring of stages carries codes and scales: `full` collects the TMA bytes
 // and the scale warps of both SMs, `empty` comes from the MMAs' commit.
 //
@@ -959,10 +960,11 @@ __device__ void gemm_epilogue(const GroupedGemmParams& p, const GemmSmem& m, con
             if (tile.n0 + c < p.N && rows > 0) put(Bf16(), w, tile.n0 + c);
           }))
         return;
-    } else for (int seg = 0; seg < segments; ++seg, ++n, add = true) {
+    } else for (int seg = 0; seg < segments; ++seg, ++n, add = true) {   // (not compiled otherwise)
       if (seg && lane == 0) tc::bulk_wait();   // the stores that it adds to are done
       const int b = n & 1;
-      if (!__all_sync(kFull, tc::sleep<C::kOrder>(m.d_full + b, (uint32_t)(n >> 1) & 1u)) || gemm_aborted(m)) {
+      if (!__all_sync(kFull, tc::sleep<C::kOrder>(m.d_full + b, (uint32_t)(n >> 1) & 1u)) ||
+          gemm_aborted(m)) {
         gemm_abort(p, m);
         return;
       }

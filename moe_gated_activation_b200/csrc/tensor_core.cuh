@@ -185,8 +185,9 @@ __device__ __forceinline__ void prefetch_map(const void* tmap) {
 }
 
 // Bulk tensor stores from shared memory and (add_*: fp32, rounded to nearest,
-// subnormals kept: held to by the tests) additions to what the output holds; bulk_wait_read: the
-// ones committed have read their shared memory, bulk_wait: they are done.
+// subnormals kept: held to by the tests) additions to what the output holds;
+// bulk_wait_read: the ones committed have read their shared memory, bulk_wait:
+// they are done.
 __device__ __forceinline__ void store_2d(const void* tmap, const void* src, int x, int y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];"
                ::"l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_addr(src)), "r"(x), "r"(y)
@@ -224,18 +225,19 @@ __device__ __forceinline__ void bulk_wait() {
 // Bounded waits (the global timer, one second).  spin: without suspending,
 // for the single warps that feed the tensor cores, whose wake-up latency
 // counts.
-#define MOEACT_WAIT_FORM(NAME, FORM, HINT)                                              \
-  template <Order O>                                                                    \
-  __device__ __forceinline__ bool NAME(uint64_t* bar, uint32_t parity) {                \
-    uint32_t ok;                                                                        \
-    if constexpr (O == kSm) MOEACT_WAIT_ASM(FORM "shared::cta.b64", HINT);              \
-    else if constexpr (O == kPair) MOEACT_WAIT_ASM(FORM "relaxed.cluster.shared::cta.b64", HINT); \
-    else MOEACT_WAIT_ASM(FORM "acquire.cluster.shared::cta.b64", HINT);                 \
-    return ok != 0;                                                                     \
-  }
-#define MOEACT_WAIT_ASM(FORM, HINT)                                                      \
-  asm volatile("{ .reg .pred p; " FORM " p, [%1], %2" HINT "; selp.u32 %0, 1, 0, p; }"   \
+#define MOEACT_WAIT_ASM(FORM, SCOPE, HINT)                                               \
+  asm volatile("{ .reg .pred p; " FORM SCOPE "shared::cta.b64 p, [%1], %2" HINT          \
+               "; selp.u32 %0, 1, 0, p; }"                                               \
                : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity), "r"(kWaitHintNs) : "memory")
+#define MOEACT_WAIT_FORM(NAME, FORM, HINT)                                               \
+  template <Order O>                                                                     \
+  __device__ __forceinline__ bool NAME(uint64_t* bar, uint32_t parity) {                 \
+    uint32_t ok;                                                                         \
+    if constexpr (O == kSm) MOEACT_WAIT_ASM(FORM, "", HINT);                             \
+    else if constexpr (O == kPair) MOEACT_WAIT_ASM(FORM, "relaxed.cluster.", HINT);      \
+    else MOEACT_WAIT_ASM(FORM, "acquire.cluster.", HINT);                                \
+    return ok != 0;                                                                      \
+  }
 MOEACT_WAIT_FORM(test, "mbarrier.test_wait.parity.", "")
 MOEACT_WAIT_FORM(test_sleep, "mbarrier.try_wait.parity.", ", %3")
 #undef MOEACT_WAIT_FORM
